@@ -27,13 +27,18 @@ EXPORTS = ["eidm_abi_version", "eidm_last_error", "eidm_query", "eidm_route_topk
            "eidm_validate_ids", "eidm_plan_create", "eidm_plan_destroy", "eidm_plan_freeze",
            "eidm_plan_route", "eidm_calibration_workspace_bytes", "eidm_calibrate",
            "eidm_matmul_id_planned", "eidm_moe_ffn_scratch_bytes", "eidm_moe_ffn", "eidm_matmul_id_noalloc",
-           "eidm_last_dispatch", "eidm_plan_set_limits"]
+           "eidm_last_dispatch", "eidm_plan_set_limits", "eidm_moe_ffn_decode_scratch_bytes", "eidm_moe_ffn_decode",
+           "eidm_lora_linear_scratch_bytes", "eidm_lora_linear"]
 
 # eidm_kernel (include/eidm.h): kernels a call can launch
 KERNELS = {1: "route", 2: "map_one_pass", 3: "map_histogram", 4: "map_scatter", 5: "direct",
            6: "grouped_16x16", 7: "grouped_stream", 8: "grouped_job", 9: "combine",
            10: "fused_decode", 11: "silu_mul", 12: "validate", 13: "proof", 14: "split_x",
-           15: "direct_split16", 16: "grouped_split16", 17: "map_split_x"}
+           15: "direct_split16", 16: "grouped_split16", 17: "map_split_x",
+           18: "decode_gate_up", 19: "decode_down", 20: "lora_shrink", 21: "lora_expand"}
+DECODE_MAX_TOKENS = 64
+LORA_MAX_RANK = 256
+NO_ADAPTER = 0xFFFFFFFF
 MAX_RECORDED_LAUNCHES = 16
 
 
@@ -59,6 +64,37 @@ class FfnShape(ctypes.Structure):
                 ("m", ctypes.c_uint32), ("hidden", ctypes.c_uint32), ("inter", ctypes.c_uint32),
                 ("top_k", ctypes.c_uint32), ("n_experts", ctypes.c_uint32), ("reserved0", ctypes.c_uint32),
                 ("gate_up_stride_bytes", ctypes.c_uint64), ("down_stride_bytes", ctypes.c_uint64)]
+
+
+class LoraShape(ctypes.Structure):
+    """eidm_lora_shape (include/eidm.h)."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("weight_dtype", ctypes.c_int32),
+                ("adapter_dtype", ctypes.c_int32), ("arith", ctypes.c_int32),
+                ("m", ctypes.c_uint32), ("n", ctypes.c_uint32), ("k", ctypes.c_uint32),
+                ("n_adapters", ctypes.c_uint32), ("max_rank", ctypes.c_uint32), ("reserved0", ctypes.c_uint32),
+                ("a_stride_bytes", ctypes.c_uint64), ("b_stride_bytes", ctypes.c_uint64)]
+
+
+def _itemsize(dtype: int) -> int:
+    return 4 if dtype == F32 else 2
+
+
+def make_ffn_shape(dtype: int, m: int, hidden: int, inter: int, top_k: int, n_experts: int,
+                   gate_up_stride: int | None = None, down_stride: int | None = None) -> FfnShape:
+    """The strides (bytes between experts) default to densely packed experts."""
+    dense = hidden * inter * _itemsize(dtype)
+    return FfnShape(ctypes.sizeof(FfnShape), dtype, m, hidden, inter, top_k, n_experts, 0,
+                    dense if gate_up_stride is None else gate_up_stride,
+                    dense if down_stride is None else down_stride)
+
+
+def make_lora_shape(weight_dtype: int, adapter_dtype: int, m: int, n: int, k: int, n_adapters: int, max_rank: int,
+                    arith: int = ARITH_F32, a_stride: int | None = None, b_stride: int | None = None) -> LoraShape:
+    """The strides (bytes between adapters) default to densely packed adapters."""
+    size = _itemsize(adapter_dtype)
+    return LoraShape(ctypes.sizeof(LoraShape), weight_dtype, adapter_dtype, arith, m, n, k, n_adapters, max_rank, 0,
+                     max_rank * k * size if a_stride is None else a_stride,
+                     n * max_rank * size if b_stride is None else b_stride)
 
 
 def ffn_shape_of(fw) -> FfnShape:
@@ -171,6 +207,43 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream) -> int:
+    if isinstance(stream, int):
+        return stream
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _address(name: str, t, nbytes: int, device: int, dtype=None) -> int | None:
+    """The device address of a call's buffer; refuses what the call cannot use
+    (a host, strided, short or differently typed tensor, or one of another
+    device than the call's)."""
+    if t is None or isinstance(t, int):
+        return t  # absent, or a raw address that the caller vouches for
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor of the current device ({device}), not of {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
+    return t.data_ptr()
+
+
+def _extent(t) -> int:
+    """The bytes vouched for: a tensor's own, none for an absent one.  (A raw
+    address has no extent that this binding could pass on.)"""
+    if isinstance(t, int):
+        raise ValueError("a weight must be a tensor")
+    return 0 if t is None else t.nbytes
+
+
+def _id_address(name: str, t, nbytes: int, device: int) -> int | None:
+    if isinstance(t, torch.Tensor) and t.dtype not in (torch.int32, torch.uint32):
+        raise ValueError(f"{name} must hold 32-bit ids, not {t.dtype}")
+    return _address(name, t, nbytes, device)
+
+
 class Library:
     def __init__(self, path: str = LIB_PATH):
         if not os.path.exists(path):
@@ -225,6 +298,14 @@ class Library:
         L.eidm_moe_ffn.restype = i32
         L.eidm_moe_ffn.argtypes = [ctypes.POINTER(FfnShape), i32, P, P, u64, P, u64, P, P, P, i32, P, P, P, P,
                                    u64, P, ctypes.POINTER(ctypes.c_int)]
+        L.eidm_moe_ffn_decode_scratch_bytes.restype = u64
+        L.eidm_moe_ffn_decode_scratch_bytes.argtypes = [ctypes.POINTER(FfnShape)]
+        L.eidm_moe_ffn_decode.restype = i32
+        L.eidm_moe_ffn_decode.argtypes = [P, P, P, u64, P, u64, P, P, P, i32, P, P, P, P, u64, P]
+        L.eidm_lora_linear_scratch_bytes.restype = u64
+        L.eidm_lora_linear_scratch_bytes.argtypes = [ctypes.POINTER(LoraShape)]
+        L.eidm_lora_linear.restype = i32
+        L.eidm_lora_linear.argtypes = [P, P, u64, P, P, u64, P, u64, P, P, P, P, P, P, u64, P]
         L.eidm_moe_forward.restype = i32
         L.eidm_moe_forward.argtypes = [ctypes.POINTER(Shape), i32, P, u64, P, P, P, i32, P, P, P, P,
                                        P, u64, P, ctypes.POINTER(ctypes.c_int)]
@@ -375,6 +456,58 @@ class Library:
                                           int(renormalize), _ptr(ids), _ptr(gates), _ptr(out), _ptr(scratch),
                                           _nbytes(scratch), _stream(stream), ctypes.byref(taken)))
         return taken.value
+
+    def moe_ffn_decode_scratch_bytes(self, shape: FfnShape) -> int:
+        """Scratch bytes of moe_ffn_decode; raises when the shape is refused."""
+        n = self.lib.eidm_moe_ffn_decode_scratch_bytes(ctypes.byref(shape))
+        if not n:
+            raise EidmError(E_INVALID, self.last_error())
+        return n
+
+    def moe_ffn_decode(self, shape: FfnShape, w_gate, w_up, w_down, x, logits, bias, ids, gates, out, scratch,
+                       renormalize: bool = True, stream=None) -> None:
+        """The expert FFN of up to DECODE_MAX_TOKENS tokens: moe_ffn's results
+        bit for bit, each touched expert's weights read once."""
+        dev = torch.cuda.current_device()
+        m, top_k, f32 = shape.m, shape.top_k, torch.float32
+        act, routed = 4 * m * shape.hidden, 4 * m * top_k
+        # the C call checks the weights' and the scratch's extents
+        rc = self.lib.eidm_moe_ffn_decode(
+            ctypes.addressof(shape), _address("w_gate", w_gate, 0, dev), _address("w_up", w_up, 0, dev),
+            min(_extent(w_gate), _extent(w_up)), _address("w_down", w_down, 0, dev), _extent(w_down),
+            _address("x", x, act, dev, f32), _address("logits", logits, 4 * m * shape.n_experts, dev, f32),
+            _address("bias", bias, 4 * shape.n_experts, dev, f32), int(renormalize),
+            _id_address("ids", ids, routed, dev), _address("gates", gates, routed, dev, f32),
+            _address("out", out, act, dev, f32), _address("scratch", scratch, 0, dev), _extent(scratch),
+            _raw_stream(stream))
+        if rc:
+            self._check(rc)
+
+    def lora_linear_scratch_bytes(self, shape: LoraShape) -> int:
+        """Scratch bytes of lora_linear; raises when the shape is refused."""
+        n = self.lib.eidm_lora_linear_scratch_bytes(ctypes.byref(shape))
+        if not n:
+            raise EidmError(E_INVALID, self.last_error())
+        return n
+
+    def lora_linear(self, shape: LoraShape, weights, base, adapter_a, adapter_b, ranks, scales, input, adapter_ids,
+                    output, scratch, stream=None) -> None:
+        """output = (weights . input, or base) + each row's own adapter's
+        scaled low-rank product; exactly one of weights and base is given."""
+        dev = torch.cuda.current_device()
+        m, f32 = shape.m, torch.float32
+        rows, per_adapter = 4 * m * shape.n, 4 * shape.n_adapters
+        # the C call checks the weights', adapters' and the scratch's extents
+        rc = self.lib.eidm_lora_linear(
+            ctypes.addressof(shape), _address("weights", weights, 0, dev), _extent(weights),
+            _address("base", base, rows, dev, f32), _address("adapter_a", adapter_a, 0, dev), _extent(adapter_a),
+            _address("adapter_b", adapter_b, 0, dev), _extent(adapter_b),
+            _id_address("ranks", ranks, per_adapter, dev), _address("scales", scales, per_adapter, dev, f32),
+            _address("input", input, 4 * m * shape.k, dev, f32), _id_address("adapter_ids", adapter_ids, 4 * m, dev),
+            _address("output", output, rows, dev, f32), _address("scratch", scratch, 0, dev), _extent(scratch),
+            _raw_stream(stream))
+        if rc:
+            self._check(rc)
 
 
 class Plan:

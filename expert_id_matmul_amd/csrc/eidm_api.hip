@@ -70,11 +70,28 @@ int api_ok() {
     return EIDM_OK;
 }
 
+namespace {
+std::atomic<int> g_cus[64];
+}
+
+int device_cus() {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    int v = g_cus[dev].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+        cus = 256;
+    g_cus[dev].store(cus, std::memory_order_relaxed);
+    return cus;
+}
+
 }  // namespace eidm
 
 namespace {
 
 using eidm::api_fail;
+using eidm::device_cus;
 int ok() { return eidm::api_ok(); }
 
 bool mul_ok(uint64_t a, uint64_t b, uint64_t* out) {
@@ -217,20 +234,6 @@ int resolve_route(const eidm_shape* s, const Plan& p, int route, bool scratch_gi
 }
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
-
-std::atomic<int> g_cus[64];
-
-int device_cus() {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    int v = g_cus[dev].load(std::memory_order_relaxed);
-    if (v > 0) return v;
-    int cus = 0;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-        cus = 256;
-    g_cus[dev].store(cus, std::memory_order_relaxed);
-    return cus;
-}
 
 int device_fail(hipError_t err, const char* what) {
     return api_fail(EIDM_E_DEVICE, "%s: %s", what, hipGetErrorString(err));

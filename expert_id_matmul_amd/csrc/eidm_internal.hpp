@@ -15,6 +15,10 @@ constexpr uint32_t kMaxExperts = 2048;
 constexpr uint32_t kMaxRouterTopK = 64;
 // fused route -> Direct -> combine: one wavefront per slot in a block
 constexpr uint32_t kMaxMoeDirectTopK = 16;
+// the few-token expert FFN: its id -> row map and its output rows sit in LDS
+constexpr uint32_t kMaxDecodeTokens = EIDM_DECODE_MAX_TOKENS;
+constexpr uint32_t kMaxDecodeTopK = 16;
+constexpr uint32_t kMaxLoraRank = EIDM_LORA_MAX_RANK;
 
 struct MatmulArgs {
     int dtype;
@@ -106,6 +110,35 @@ bool moe_direct_supported(uint32_t top_k, uint32_t n_experts);
 // synchronous: waits for `stream`; *first_bad = smallest bad routed index or -1
 hipError_t run_validate(const uint32_t* ids, uint32_t m, uint32_t top_k, uint32_t n_experts, int distinct,
                         hipStream_t stream, int* first_bad);
+// The expert FFN of a few tokens (moe_decode.hip): ids and gates are routed
+// already; h is [m*top_k][h_stride] f32 scratch.
+struct MoeDecodeArgs {
+    int dtype;
+    uint32_t m, hidden, inter, top_k, n_experts, h_stride;
+    uint64_t gate_up_stride, down_stride;
+    const uint8_t *w_gate, *w_up, *w_down;
+    const float* x;
+    const uint32_t* ids;
+    const float* gates;
+    float *h, *out;
+};
+hipError_t launch_moe_decode(const MoeDecodeArgs& a, int device_cus, hipStream_t stream);
+// compute units of the current device
+int device_cus();
+// Low-rank adapters (lora.hip): v [m][v_stride] f32 scratch; base may be
+// output itself.
+struct LoraArgs {
+    int dtype;  // of the adapters
+    uint32_t m, n, k, n_adapters, max_rank, v_stride;
+    uint64_t a_stride, b_stride;
+    const uint8_t *a, *b;
+    const uint32_t *ranks, *ids;
+    const float *scales, *x, *base;
+    float *v, *out;
+    uint32_t* zero_ids;  // [m] ids of the shared projection, written by the shrink (or null)
+};
+hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream);
+hipError_t launch_lora_expand(const LoraArgs& a, int device_cus, hipStream_t stream);
 // a.ids is ignored: the kernel writes the picks to `ids` and reads them itself
 hipError_t launch_moe_direct(const MatmulArgs& a, const float* logits, const float* bias, int renormalize,
                              uint32_t* ids, float* gates, float* out, int device_cus, hipStream_t stream);

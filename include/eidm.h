@@ -161,8 +161,12 @@ typedef enum eidm_kernel {
     EIDM_KERNEL_SPLIT_X = 14,       /* split-16: activations into three parts        */
     EIDM_KERNEL_DIRECT_SPLIT16 = 15,  /* split-16 Direct                             */
     EIDM_KERNEL_GROUPED_SPLIT16 = 16, /* split-16 Grouped                            */
-    EIDM_KERNEL_MAP_SPLIT_X = 17      /* split-16 Grouped: the one-launch map and the
+    EIDM_KERNEL_MAP_SPLIT_X = 17,     /* split-16 Grouped: the one-launch map and the
                                          activation split in one launch              */
+    EIDM_KERNEL_DECODE_GATE_UP = 18,  /* few-token FFN: gate and up products, silu * up */
+    EIDM_KERNEL_DECODE_DOWN = 19,     /* few-token FFN: down product and combine      */
+    EIDM_KERNEL_LORA_SHRINK = 20,     /* adapters: v = A x                            */
+    EIDM_KERNEL_LORA_EXPAND = 21      /* adapters: y = base + scale * B v             */
 } eidm_kernel;
 
 /* One kernel launch: which kernel and its launch geometry (1-D grid of
@@ -404,6 +408,89 @@ int eidm_moe_ffn(const eidm_ffn_shape* shape, int route, const void* w_gate, con
                  uint64_t gate_up_bytes, const void* w_down, uint64_t down_bytes, const float* x,
                  const float* logits, const float* bias, int renormalize, uint32_t* ids, float* gates,
                  float* out, void* scratch, uint64_t scratch_bytes, void* stream, int* route_taken);
+
+/* Most tokens eidm_moe_ffn_decode takes, and most adapter ranks
+ * eidm_lora_linear takes. */
+#define EIDM_DECODE_MAX_TOKENS 64
+#define EIDM_LORA_MAX_RANK 256
+
+/*
+ * The expert FFN of a few tokens (a decode step of up to
+ * EIDM_DECODE_MAX_TOKENS requests): the computation, the arguments and the
+ * bits of eidm_moe_ffn, reading each touched expert's three matrices once
+ * however many of the tokens chose it, in one launch for routing, gate, up
+ * and silu * up, and one for down and combine.
+ * Requires m <= EIDM_DECODE_MAX_TOKENS, top_k <= 16 and the router's limits
+ * (else EIDM_E_UNSUPPORTED).  Weights need the scalar's alignment only; no
+ * buffer may overlap another.  scratch: device, 256-byte aligned, at least
+ * eidm_moe_ffn_decode_scratch_bytes(shape) bytes; its contents need no
+ * preparation and mean nothing afterwards.
+ */
+uint64_t eidm_moe_ffn_decode_scratch_bytes(const eidm_ffn_shape* shape);
+
+int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const void* w_up,
+                        uint64_t gate_up_bytes, const void* w_down, uint64_t down_bytes, const float* x,
+                        const float* logits, const float* bias, int renormalize, uint32_t* ids,
+                        float* gates, float* out, void* scratch, uint64_t scratch_bytes, void* stream);
+
+/* The adapter id of a row that has no adapter. */
+#define EIDM_NO_ADAPTER 0xffffffffu
+
+/*
+ * Low-rank adapters of many requests at once beside a shared projection:
+ * for every row t with adapter a = adapter_ids[t] of rank r = ranks[a]
+ *   v[i]      = sum_c A_a[i, c] * x[t, c],   i < r   (the fixed order of
+ *               eidm_matmul_id's F32 arithmetic)
+ *   u[j]      = sum_i B_a[j, i] * v[i]               (f32 fma from +0, i
+ *               ascending)
+ *   out[t, j] = fma(scales[a], u[j], base[t, j])
+ * The adapters are selected per row as experts are (mlx-native
+ * dense_matmul_id_auto.rs: one weight of a stack per row id).  A row's
+ * result depends on no other row of the call.
+ *
+ * weights       the shared projection W [n, k] (device, weight_dtype, k
+ *               contiguous, weight_bytes the extent vouched for): base = W x,
+ *               the bits of eidm_matmul_id with one expert in the shape's
+ *               arith (SPLIT16 with its conditions there); NULL when `base`
+ *               is given
+ * base          device f32 [m, n], products the adapters are added to; may be
+ *               `output` itself.  Exactly one of weights and base is given.
+ * adapter_a     device, adapter_dtype, adapter a's A [max_rank, k] at byte
+ *               a * a_stride_bytes
+ * adapter_b     device, adapter_dtype, adapter a's B [n, max_rank] at byte
+ *               a * b_stride_bytes
+ * ranks         device u32 [n_adapters], or NULL: every adapter has max_rank.
+ *               A rank above max_rank counts as max_rank; elements of A and B
+ *               past the rank are not used.  Rank 0 leaves the row's base.
+ * scales        device f32 [n_adapters], or NULL: 1
+ * input         device f32 [m, k]
+ * adapter_ids   device u32 [m].  EIDM_NO_ADAPTER leaves the row's base; any
+ *               other id >= n_adapters makes the row quiet NaN.
+ * output        device f32 [m, n]; overlaps nothing but, whole, base
+ * scratch       device, 256-byte aligned, at least
+ *               eidm_lora_linear_scratch_bytes(shape) bytes; its contents
+ *               need no preparation and mean nothing afterwards
+ * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m and n*... as
+ * for eidm_matmul_id (else EIDM_E_UNSUPPORTED).
+ */
+typedef struct eidm_lora_shape {
+    uint32_t struct_size;    /* sizeof(eidm_lora_shape) */
+    int32_t weight_dtype;    /* eidm_dtype of W (not read when base is given) */
+    int32_t adapter_dtype;   /* eidm_dtype of A and B   */
+    int32_t arith;           /* eidm_arith of W x       */
+    uint32_t m, n, k;        /* rows, output columns, reduction length */
+    uint32_t n_adapters, max_rank, reserved0;
+    uint64_t a_stride_bytes; /* bytes between adapters of A */
+    uint64_t b_stride_bytes; /* bytes between adapters of B */
+} eidm_lora_shape;
+
+/* Host-only: scratch bytes eidm_lora_linear needs (0 if the shape is invalid). */
+uint64_t eidm_lora_linear_scratch_bytes(const eidm_lora_shape* shape);
+
+int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t weight_bytes, const float* base,
+                     const void* adapter_a, uint64_t a_bytes, const void* adapter_b, uint64_t b_bytes,
+                     const uint32_t* ranks, const float* scales, const float* input, const uint32_t* adapter_ids,
+                     float* output, void* scratch, uint64_t scratch_bytes, void* stream);
 
 /*
  * Activation-time route calibration and the frozen plan (mlx-native

@@ -57,6 +57,8 @@ def _load():
     lib.oracle_combine.argtypes = [u32, u32, u32, P, P, P]
     lib.oracle_moe_ffn.restype = i32
     lib.oracle_moe_ffn.argtypes = [i32, u32, u32, u32, u32, u32, u64, u64, P, P, P, P, P, P, P, P]
+    lib.oracle_lora_linear.restype = i32
+    lib.oracle_lora_linear.argtypes = [i32, i32, u32, u32, u32, u32, u32, u64, u64, P, P, P, P, P, P, P, P, P]
     lib.oracle_map.restype = i32
     lib.oracle_map.argtypes = [P, u64, u32, P, P, P]
     _lib = lib
@@ -203,3 +205,31 @@ def moe_ffn(dtype: int, m: int, hidden: int, inter: int, top_k: int, n_experts: 
     if rc != 0:
         raise ValueError(f"oracle_moe_ffn failed ({rc})")
     return out, h
+
+
+def lora_linear(w_dtype: int, a_dtype: int, m: int, n: int, k: int, n_adapters: int, max_rank: int, a_stride: int,
+                b_stride: int, w: np.ndarray | None, base: np.ndarray | None, a: np.ndarray, b: np.ndarray,
+                ranks: np.ndarray | None, scales: np.ndarray | None, x: np.ndarray, ids: np.ndarray) -> np.ndarray:
+    """-> out f64 [m, n]: a projection (w, or its given result base) with a low-rank adapter per row."""
+    a, b = _c(a, np.uint8).reshape(-1), _c(b, np.uint8).reshape(-1)
+    assert a.size >= required_weight_bytes(a_dtype, max_rank, k, n_adapters, a_stride)
+    assert b.size >= required_weight_bytes(a_dtype, n, max_rank, n_adapters, b_stride)
+    if w is not None:
+        w = _c(w, np.uint8).reshape(-1)
+        assert w.size >= n * k * (4 if w_dtype == F32 else 2)
+    if base is not None:
+        base = _c(base, np.float64)
+        assert base.size == m * n
+    ranks = None if ranks is None else _c(ranks, np.uint32)
+    scales = None if scales is None else _c(scales, np.float32)
+    x, ids = _c(x, np.float32), _c(ids, np.uint32)
+    assert x.size == m * k and ids.size == m
+    assert ranks is None or ranks.size == n_adapters
+    assert scales is None or scales.size == n_adapters
+    out = np.empty((m, n), dtype=np.float64)
+    rc = _load().oracle_lora_linear(w_dtype, a_dtype, m, n, k, n_adapters, max_rank, a_stride, b_stride, _ptr(w),
+                                    _ptr(base), _ptr(a), _ptr(b), _ptr(ranks), _ptr(scales), _ptr(x), _ptr(ids),
+                                    _ptr(out))
+    if rc != 0:
+        raise ValueError(f"oracle_lora_linear: {rc}")
+    return out

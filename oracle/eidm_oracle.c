@@ -420,3 +420,48 @@ int oracle_moe_ffn(int dtype, uint32_t m, uint32_t hidden, uint32_t inter, uint3
     free(h);
     return 0;
 }
+
+/*
+ * Low-rank adapters beside a shared projection: out[t, j] = base[t, j] +
+ * scale_a * sum_i B_a[j, i] * (sum_c A_a[i, c] * x[t, c]), a = ids[t], i below
+ * min(ranks[a], max_rank); base = W x, or given.  id 0xffffffff: base alone;
+ * any other id >= n_adapters: a NaN row.  ranks, scales: NULL = max_rank, 1.
+ */
+int oracle_lora_linear(int w_dtype, int a_dtype, uint32_t m, uint32_t n, uint32_t k, uint32_t n_adapters,
+                       uint32_t max_rank, uint64_t a_stride, uint64_t b_stride, const void* w, const double* base,
+                       const void* a, const void* b, const uint32_t* ranks, const float* scales, const float* x,
+                       const uint32_t* ids, double* out) {
+    int ws = dtype_size(w_dtype), as = dtype_size(a_dtype);
+    if (!as || (w && !ws) || (w == NULL) == (base == NULL) || !m || !n || !k || !n_adapters || !max_rank) return -1;
+    double* v = (double*)malloc(sizeof(double) * max_rank);
+    if (!v) return -2;
+    for (uint64_t t = 0; t < m; ++t) {
+        uint32_t id = ids[t];
+        uint32_t rank = 0;
+        if (id < n_adapters) {
+            rank = ranks && ranks[id] < max_rank ? ranks[id] : max_rank;
+            const uint8_t* ad = (const uint8_t*)a + (uint64_t)id * a_stride;
+            for (uint32_t i = 0; i < rank; ++i) {
+                v[i] = 0.0;
+                for (uint64_t c = 0; c < k; ++c)
+                    v[i] += oracle_widen(a_dtype, ad + ((uint64_t)i * k + c) * as) * (double)x[t * k + c];
+            }
+        }
+        for (uint64_t j = 0; j < n; ++j) {
+            double y = 0.0, u = 0.0;
+            if (base) {
+                y = base[t * n + j];
+            } else {
+                for (uint64_t c = 0; c < k; ++c)
+                    y += oracle_widen(w_dtype, (const uint8_t*)w + (j * k + c) * ws) * (double)x[t * k + c];
+            }
+            for (uint32_t i = 0; i < rank; ++i)
+                u += oracle_widen(a_dtype, (const uint8_t*)b + (uint64_t)id * b_stride + (j * max_rank + i) * as) * v[i];
+            if (rank) y += (scales ? (double)scales[id] : 1.0) * u;
+            if (id >= n_adapters && id != 0xffffffffu) y = NAN;
+            out[t * n + j] = y;
+        }
+    }
+    free(v);
+    return 0;
+}
