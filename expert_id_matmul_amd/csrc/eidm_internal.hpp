@@ -18,6 +18,7 @@ constexpr uint32_t kMaxMoeDirectTopK = 16;
 // the few-token expert FFN: its id -> row map and its output rows sit in LDS
 constexpr uint32_t kMaxDecodeTokens = EIDM_DECODE_MAX_TOKENS;
 constexpr uint32_t kMaxDecodeTopK = 16;
+constexpr uint32_t kMaxDecodeRow = 32768;
 constexpr uint32_t kMaxLoraRank = EIDM_LORA_MAX_RANK;
 
 struct MatmulArgs {
@@ -110,17 +111,17 @@ bool moe_direct_supported(uint32_t top_k, uint32_t n_experts);
 // synchronous: waits for `stream`; *first_bad = smallest bad routed index or -1
 hipError_t run_validate(const uint32_t* ids, uint32_t m, uint32_t top_k, uint32_t n_experts, int distinct,
                         hipStream_t stream, int* first_bad);
-// The expert FFN of a few tokens (moe_decode.hip): ids and gates are routed
-// already; h is [m*top_k][h_stride] f32 scratch.
+// The expert FFN of a few tokens (moe_decode.hip); h [m*top_k][inter] and
+// y [m*top_k][hidden] are f32 scratch.
 struct MoeDecodeArgs {
     int dtype;
-    uint32_t m, hidden, inter, top_k, n_experts, h_stride;
+    uint32_t m, hidden, inter, top_k, n_experts;
     uint64_t gate_up_stride, down_stride;
     const uint8_t *w_gate, *w_up, *w_down;
-    const float* x;
-    const uint32_t* ids;
-    const float* gates;
-    float *h, *out;
+    const float *x, *logits, *bias;
+    int renormalize;
+    uint32_t* ids;
+    float *gates, *h, *y, *out;
 };
 hipError_t launch_moe_decode(const MoeDecodeArgs& a, int device_cus, hipStream_t stream);
 // compute units of the current device

@@ -38,9 +38,23 @@ __device__ __forceinline__ FewMap few_map_at(uint32_t* lds, uint32_t rows, uint3
 }
 
 // The whole block takes part; ids that are >= n_ids have no list.  The map
-// is ready for every thread on return.
-__device__ __forceinline__ void few_map_build(const FewMap& f, const uint32_t* ids, uint32_t rows, uint32_t n_ids) {
+// is ready for every thread on return.  One token's ids (tokens == 1) are
+// distinct and below n_ids: they keep their own order, one row each.
+__device__ __forceinline__ void few_map_build(const FewMap& f, const uint32_t* ids, uint32_t rows, uint32_t n_ids,
+                                              uint32_t tokens) {
     const uint32_t tid = threadIdx.x, nt = blockDim.x;
+    if (tokens == 1) {
+        for (uint32_t r = tid; r <= rows; r += nt) {
+            f.off[r] = r;
+            if (r < rows) {
+                f.id[r] = ids[r];
+                f.row[r] = r;
+            }
+        }
+        if (tid == 0) *f.used = rows;
+        __syncthreads();
+        return;
+    }
     for (uint32_t e = tid; e < n_ids; e += nt) f.start[e] = 0;
     __syncthreads();
     for (uint32_t r = tid; r < rows; r += nt) {

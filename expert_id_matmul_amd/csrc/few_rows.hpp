@@ -1,6 +1,6 @@
-// few_rows.hpp -- one wavefront's product of a few activation rows with 4*C
-// weight rows (output columns), in the library's fixed reduction order; used
-// by the few-token expert layer and by the adapters' low-rank products.
+// few_rows.hpp -- one wavefront's product of a few activation rows, staged in
+// LDS, with 4*C weight rows (output columns), in the library's fixed
+// reduction order; used by the few-token expert layer and by the adapters.
 //
 // A weight row is read once for up to 16 activation rows.  The lane layout is
 // that of the 4x4x1 matrix-core step (eidm_device.hpp): lane 4b+i holds, per
@@ -10,11 +10,14 @@
 // takes the same step on the vector ALU (one lane per slice and column: half
 // the issue cycles, the same bits).
 //
-// Rounds run through a ring of D register slots, as in direct_wave.hpp: all
-// D rounds ahead are in flight, each wait is for the oldest slot only.
-// Rows need no 16-byte alignment: the loads are declared with the scalar's
-// alignment, which global loads take at any address; only the last, partial
-// round is masked (per granule; a granule cut by k is read element-wise).
+// What bounds it is the weight stream, so the registers hold weights only: a
+// ring of D rounds in flight, each wait for the oldest one, as in
+// direct_wave.hpp.  With the activations in the ring too (8 registers a round
+// for every four rows) the kernel spilled, and a spill's reload waits for the
+// whole ring; in LDS they cost no register and no place in the load queue.
+// Weight rows need no 16-byte alignment: the loads are declared with the
+// scalar's alignment, which global loads take at any address; only the last,
+// partial round is masked (a granule cut by k is read element-wise).
 #pragma once
 
 #include "eidm_device.hpp"
@@ -26,11 +29,34 @@ typedef unsigned int fr_u32x4 __attribute__((ext_vector_type(4)));
 typedef fr_u32x4 fr_u32x4_a2 __attribute__((aligned(2)));
 typedef f32x4 fr_f32x4_a4 __attribute__((aligned(4)));
 
-template <int DT, int C, int RG>
-struct FewSlot {
-    fr_u32x4 w[C][DtypeSize<DT>::value / 2];
-    f32x4 x[RG][2];
-};
+constexpr int kFewRows = 16;  // activation rows of one pass over a weight row
+
+// An activation row in LDS: per 128-element round the first halves of its 16
+// granules, then the second halves, zero past k; rows are 64 bytes off a
+// multiple of the 256-byte bank span, so the four rows of a row group that a
+// 16-byte read takes together fall on different banks.
+__host__ __device__ constexpr uint32_t few_row_floats(uint32_t k) { return (k + 127) / 128 * 128 + 16; }
+
+// Stages rows row_of(0 .. count-1) of k f32 elements (4-byte aligned) as LDS
+// rows 0 .. count-1; the whole block takes part.
+template <typename RowOf>
+__device__ __forceinline__ void few_rows_stage(float* xs, uint32_t count, uint32_t k, RowOf row_of) {
+    const uint32_t pieces = (k + 127) / 128 * 32;  // 16-byte pieces per row
+    const uint32_t stride = few_row_floats(k);
+    for (uint32_t i = threadIdx.x; i < count * pieces; i += blockDim.x) {
+        const uint32_t r = i / pieces, p = i % pieces;
+        const float* src = row_of(r) + p * 4;
+        f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+        if (p * 4 + 4 <= k) {
+            v = *reinterpret_cast<const fr_f32x4_a4*>(src);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (p * 4 + j < k) v[j] = src[j];
+        }
+        *reinterpret_cast<f32x4*>(xs + (size_t)r * stride + (p / 32) * 128 + (p & 1) * 64 + (p % 32) / 2 * 4) = v;
+    }
+}
 
 template <int DT>
 __device__ __forceinline__ void few_widen(const fr_u32x4 (&p)[DtypeSize<DT>::value / 2], float (&w)[kGranule]) {
@@ -46,122 +72,112 @@ __device__ __forceinline__ void few_widen(const fr_u32x4 (&p)[DtypeSize<DT>::val
     }
 }
 
-// Accumulates acc[g][c] over k.  ONE: row group 0 holds one row, every lane
-// of slice b passes that row, and acc[0][c][0] of lane 4b+i is column i's
-// slice sum; else acc[g][c][v] of lane 4b+i is (row v, column i) of slice b.
-// wrow[c], xrow[g]: this lane's weight row and activation row (the caller
-// repeats a valid row for lanes that have none).  NT: weights are read once,
-// so their loads are non-temporal.
-template <int DT, int C, int RG, int D, bool ONE, bool NT = true>
-__device__ __forceinline__ void few_rows_product(const uint8_t* const (&wrow)[C], const float* const (&xrow)[RG], int k,
-                                                 f32x4 (&acc)[RG][C]) {
+// Accumulates acc[g][c] over k.  RG row groups of four rows, xl[g] the LDS
+// row of this lane's row (row q of group g); RG = 0: one row, xl[0] in every
+// lane, and acc[0][c][0] of lane 4b+i is column i's slice sum; else
+// acc[g][c][v] of lane 4b+i is (row v, column i) of slice b.
+// wrow[c]: this lane's weight row (the caller repeats a valid one for lanes
+// that have none).  NT: weights are read once, by non-temporal loads.
+template <int DT, int C, int RG, int D, bool NT>
+__device__ __forceinline__ void few_rows_product(const uint8_t* const (&wrow)[C],
+                                                 const float* const (&xl)[RG ? RG : 1], int k,
+                                                 f32x4 (&acc)[RG ? RG : 1][C]) {
     constexpr int S = DtypeSize<DT>::value;
     constexpr int NP = S / 2;
+    constexpr int G = RG ? RG : 1;
     const int b = (threadIdx.x & 63) >> 2;
     const int full = k / kRoundK;
 
 #pragma unroll
-    for (int g = 0; g < RG; ++g)
+    for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[g][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto fetch = [&](int r, FewSlot<DT, C, RG>& s) {
-        const size_t at = (size_t)r * kRoundK + (size_t)b * kGranule;
+    struct Slot {
+        fr_u32x4 w[C][NP];
+    };
+    auto fetch = [&](int r, Slot& s) {
+        const size_t at = ((size_t)r * kRoundK + (size_t)b * kGranule) * S;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at * S + 16 * i);
+                const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at + 16 * i);
                 s.w[c][i] = NT ? __builtin_nontemporal_load(p) : *p;
             }
-#pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            s.x[g][0] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[g] + at);
-            s.x[g][1] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[g] + at + 4);
-        }
     };
-    auto step = [&](const float (&w)[C][kGranule], const float (&x)[RG][kGranule]) {
+    // four of a granule's products at a time: half the widened weights live
+    auto half = [&](int r, int h, const float (&w)[C][kGranule]) {
+        f32x4 x[G];
 #pragma unroll
-        for (int i = 0; i < kGranule; ++i)
+        for (int g = 0; g < G; ++g)
+            x[g] = *reinterpret_cast<const f32x4*>(xl[g] + r * kRoundK + h * 64 + b * 4);
 #pragma unroll
-            for (int g = 0; g < RG; ++g)
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    if constexpr (ONE)
-                        acc[g][c][0] = fma_step(x[g][i], w[c][i], acc[g][c][0]);
+                    if constexpr (RG == 0)
+                        acc[g][c][0] = fma_step(x[g][i], w[c][h * 4 + i], acc[g][c][0]);
                     else
-                        acc[g][c] = mfma_step(x[g][i], w[c][i], acc[g][c]);
+                        acc[g][c] = mfma_step(x[g][i], w[c][h * 4 + i], acc[g][c]);
                 }
     };
-    auto consume = [&](const FewSlot<DT, C, RG>& s) {
-        float w[C][kGranule], x[RG][kGranule];
+    auto consume = [&](int r, const Slot& s) {
+        float w[C][kGranule];
 #pragma unroll
         for (int c = 0; c < C; ++c) few_widen<DT>(s.w[c], w[c]);
-#pragma unroll
-        for (int g = 0; g < RG; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[g][i] = s.x[g][0][i];
-                x[g][4 + i] = s.x[g][1][i];
-            }
-        step(w, x);
+        half(r, 0, w);
+        half(r, 1, w);
     };
 
+    Slot ring[D];
     if (full > 0) {
-        FewSlot<DT, C, RG> ring[D];
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             fetch(min(d, full - 1), ring[d]);  // past the end: the last round again, never consumed
             __builtin_amdgcn_sched_barrier(0);
         }
-        int r = 0;
-        for (; r + 2 * D <= full; r += D) {
+    }
+    // the partial last round, requested behind the ring's first rounds
+    Slot tail{};
+    const int kk = full * kRoundK + b * kGranule;
+    if (kk < k) {
+        if (kk + kGranule <= k) {
+            fetch(full, tail);
+        } else {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-                consume(ring[d]);
-                fetch(r + d + D, ring[d]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < 2 * D; ++j) {
-            if (r + j < full) {
-                consume(ring[j % D]);
-                if (r + j + D < full) fetch(r + j + D, ring[j % D]);
-            }
+                for (int i = 0; i < kGranule; ++i)
+                    if (kk + i < k) {
+                        if constexpr (S == 4)
+                            tail.w[c][i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(wrow[c] + (size_t)(kk + i) * 4);
+                        else
+                            tail.w[c][0][i / 2] |=
+                                (uint32_t)*reinterpret_cast<const uint16_t*>(wrow[c] + (size_t)(kk + i) * 2) << (i % 2 * 16);
+                    }
         }
     }
-    if (full * kRoundK < k) {  // the partial last round
-        const int kk = full * kRoundK + b * kGranule;
-        float w[C][kGranule], x[RG][kGranule];
+    int r = 0;
+    for (; r + 2 * D <= full; r += D) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (kk + kGranule <= k) {
-                fr_u32x4 p[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    p[i] = *reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + (size_t)kk * S + 16 * i);
-                few_widen<DT>(p, w[c]);
-            } else {
-                load_weight_granule<DT>(wrow[c], kk, k, true, false, w[c]);
-            }
+        for (int d = 0; d < D; ++d) {
+            consume(r + d, ring[d]);
+            fetch(r + d + D, ring[d]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            if (kk + kGranule <= k) {
-                const f32x4 a = *reinterpret_cast<const fr_f32x4_a4*>(xrow[g] + kk);
-                const f32x4 c = *reinterpret_cast<const fr_f32x4_a4*>(xrow[g] + kk + 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[g][i] = a[i];
-                    x[g][4 + i] = c[i];
-                }
-            } else {
-                load_input_granule(xrow[g], kk, k, true, false, x[g]);
-            }
-        }
-        step(w, x);
     }
+#pragma unroll
+    for (int j = 0; j < 2 * D; ++j) {
+        if (r + j < full) {
+            consume(r + j, ring[j % D]);
+            if (r + j + D < full) fetch(r + j + D, ring[j % D]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (full * kRoundK < k) consume(full, tail);
 }
 
 // The 16 slice sums of (row v, column i), v = 0..3, combined in the fixed
@@ -185,6 +201,40 @@ __device__ __forceinline__ float few_rows_total(const f32x4& a) {
     t += __shfl_xor(t, 8);
     t += __shfl_xor(t, 4);
     return t;
+}
+
+// `count` (1..16) rows of LDS, rows[at .. at+count), times 4*C weight rows:
+// emit(row index, totals[C]) for every live row, in lanes that hold the
+// totals of column q = lane & 3 of each group.
+template <int DT, int C, int RG, int D, bool NT, typename Emit>
+__device__ __forceinline__ void few_rows_tile(const uint8_t* const (&wrow)[C], const float* xs, uint32_t stride,
+                                              uint32_t at, uint32_t count, int k, Emit emit) {
+    constexpr int G = RG ? RG : 1;
+    const int lane = threadIdx.x & 63;
+    const int b = lane >> 2;
+    const uint32_t q = lane & 3;
+    const float* xl[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) xl[g] = xs + (size_t)(at + (RG ? min(4 * g + q, count - 1) : 0)) * stride;
+    f32x4 acc[G][C];
+    few_rows_product<DT, C, RG, D, NT>(wrow, xl, k, acc);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = RG ? few_rows_total(acc[g][c]) : slice_tree(acc[g][c][0]);
+        const uint32_t r = RG ? 4 * g + few_row(b) : 0;
+        if (RG ? ((b & 3) == 0 && r < count) : b == 0) emit(at + r, v);
+    }
+}
+
+template <int DT, int C, int D, bool NT, typename Emit>
+__device__ __forceinline__ void few_rows_any(const uint8_t* const (&wrow)[C], const float* xs, uint32_t stride,
+                                             uint32_t at, uint32_t count, int k, Emit emit) {
+    if (count == 1) few_rows_tile<DT, C, 0, D, NT>(wrow, xs, stride, at, count, k, emit);
+    else if (count <= 4) few_rows_tile<DT, C, 1, D, NT>(wrow, xs, stride, at, count, k, emit);
+    else if (count <= 8) few_rows_tile<DT, C, 2, D, NT>(wrow, xs, stride, at, count, k, emit);
+    else few_rows_tile<DT, C, 4, D, NT>(wrow, xs, stride, at, count, k, emit);
 }
 
 }  // namespace eidm

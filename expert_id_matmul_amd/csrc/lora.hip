@@ -6,10 +6,18 @@
 //
 // An adapter is selected per row as an expert is (mlx-native 0.13.0,
 // src/ops/dense_matmul_id_auto.rs: a stack of weights, one id per row).
+//
+// Two forms of each, with the same bits.  By rows (a decode batch, where
+// rows have adapters of their own): a wavefront takes one row and streams its
+// adapter.  By tiles (prompts, where neighbouring rows share an adapter):
+// a wavefront takes 16 consecutive rows and runs once over each adapter that
+// occurs among them, so no row needs sorting and all rows are read and
+// written in their order.
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
 #include "few_rows.hpp"
+#include "rows16.hpp"
 
 namespace eidm {
 namespace {
@@ -18,77 +26,224 @@ __device__ __forceinline__ uint32_t rank_of(const LoraArgs& a, uint32_t id) {
     return a.ranks ? min(a.ranks[id], a.max_rank) : a.max_rank;
 }
 
-// One wavefront per (row, four ranks).
-template <int DT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int b = lane >> 2, q = lane & 3;
-    const uint32_t groups = (a.max_rank + 3) / 4;
-    const uint64_t jobs = (uint64_t)a.m * groups;
-    const uint64_t waves = (uint64_t)gridDim.x * 4;
+__device__ __forceinline__ float scale_of(const LoraArgs& a, uint32_t id) { return a.scales ? a.scales[id] : 1.0f; }
+
+// ids of the shared projection (one expert), written beside other work
+__device__ __forceinline__ void write_zero_ids(const LoraArgs& a) {
     if (a.zero_ids)
-        for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < a.m; i += (uint64_t)gridDim.x * 256)
+        for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.m; i += (uint64_t)gridDim.x * blockDim.x)
             a.zero_ids[i] = 0;
-    for (uint64_t job = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < jobs; job += waves) {
-        const uint32_t t = (uint32_t)(job / groups);
-        const uint32_t i0 = (uint32_t)(job % groups) * 4;
-        const uint32_t id = a.ids[t];
-        if (id >= a.n_adapters) continue;
-        const uint32_t rank = rank_of(a, id);
-        if (i0 >= rank) continue;
-        const uint32_t i = min(i0 + q, rank - 1);
-        const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride + (size_t)i * a.k * DtypeSize<DT>::value};
-        const float* const xrow[1] = {a.x + (size_t)t * a.k};
-        f32x4 acc[1][1];
-        few_rows_product<DT, 1, 1, 8, true, false>(wrow, xrow, (int)a.k, acc);
-        const float v = slice_tree(acc[0][0][0]);
-        if (b == 0 && i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v;
+}
+
+// One block per row and blockDim/64 groups of four ranks; the row is staged
+// in LDS.
+template <int DT>
+__global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t parts) {
+    extern __shared__ __align__(16) float xs[];
+    const int lane = threadIdx.x & 63;
+    const uint32_t q = lane & 3;
+    write_zero_ids(a);
+    const uint32_t t = blockIdx.x / parts, part = blockIdx.x % parts;
+    const uint32_t id = a.ids[t];
+    if (id >= a.n_adapters) return;
+    const uint32_t rank = rank_of(a, id);
+    const uint32_t waves = blockDim.x >> 6;
+    if (part * waves * 4 >= rank) return;
+    few_rows_stage(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
+    __syncthreads();
+    const uint32_t i0 = (part * waves + (threadIdx.x >> 6)) * 4;
+    if (i0 >= rank) return;
+    const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
+                                    (size_t)min(i0 + q, rank - 1) * a.k * DtypeSize<DT>::value};
+    few_rows_tile<DT, 1, 0, 16, false>(wrow, xs, 0, 0, 1, (int)a.k, [&](uint32_t, const float (&v)[1]) {
+        if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
+    });
+}
+
+// A tile of 16 consecutive rows: lane l holds row l%16's adapter (`none` for
+// a row past the last).  Calls body(id, members) for every adapter id <
+// n_adapters among them, members a bit per row of the tile.
+template <typename Body>
+__device__ __forceinline__ void for_each_adapter(uint32_t mine, uint32_t n_adapters, Body body) {
+    uint32_t left = (uint32_t)__ballot(mine < n_adapters) & 0xffffu;
+    while (left) {  // wave-uniform
+        const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)mine, __builtin_ctz(left));
+        const uint32_t members = (uint32_t)__ballot(mine == id) & 0xffffu;
+        left &= ~members;
+        body(id, members);
     }
 }
 
+// One wavefront per (16 rows, 16 ranks).
 template <int DT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a) {
+__global__ __launch_bounds__(256) void shrink_tile_kernel(LoraArgs a) {
+    const uint32_t lane = threadIdx.x & 63, i = lane & 15;
+    const uint32_t chunks = (a.max_rank + 15) / 16;
+    const uint64_t tiles = ((uint64_t)a.m + 15) / 16;
+    write_zero_ids(a);
+    for (uint64_t job = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < tiles * chunks; job += (uint64_t)gridDim.x * 4) {
+        const uint64_t t0 = job / chunks * 16;
+        const uint32_t c0 = (uint32_t)(job % chunks) * 16;
+        const uint64_t t = t0 + i < a.m ? t0 + i : a.m - 1;
+        const uint32_t mine = t0 + i < a.m ? a.ids[t] : EIDM_NO_ADAPTER;
+        for_each_adapter(mine, a.n_adapters, [&](uint32_t id, uint32_t members) {
+            const uint32_t rank = rank_of(a, id);
+            if (c0 >= rank) return;
+            const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
+                                            (size_t)min(c0 + i, rank - 1) * a.k * DtypeSize<DT>::value};
+            f32x4 total[1];
+            rows16_product<DT, 1, 8, false>(wrow, a.x + t * a.k, (int)a.k, total);
+#pragma unroll
+            for (uint32_t v = 0; v < 4; ++v) {
+                const uint32_t r = 4 * (lane >> 4) + v;
+                if ((members >> r & 1) && c0 + i < rank) a.v[(t0 + r) * a.v_stride + c0 + i] = total[0][v];
+            }
+        });
+    }
+}
+
+// Ranks i0 .. i0+7 of one row of B, widened; those past max_rank are not read.
+template <int DT>
+__device__ __forceinline__ void load_b(const uint8_t* row, uint32_t i0, uint32_t max_rank, float (&b)[kGranule]) {
     constexpr int S = DtypeSize<DT>::value;
-    const uint64_t total = (uint64_t)a.m * a.n;
-    for (uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (uint64_t)gridDim.x * 256) {
-        const uint32_t t = (uint32_t)(at / a.n), j = (uint32_t)(at % a.n);
+    if (i0 + kGranule <= max_rank) {
+        fr_u32x4 p[S / 2];
+#pragma unroll
+        for (int h = 0; h < S / 2; ++h) p[h] = *reinterpret_cast<const fr_u32x4_a2*>(row + (size_t)i0 * S + 16 * h);
+        few_widen<DT>(p, b);
+    } else {
+        load_weight_granule<DT>(row, (int)i0, (int)max_rank, true, false, b);
+    }
+}
+
+// One thread per output: the row's adapter alone.
+template <int DT>
+__global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
+    const uint32_t groups = (a.n + 255) / 256;
+    for (uint64_t job = blockIdx.x; job < (uint64_t)a.m * groups; job += gridDim.x) {
+        const uint64_t t = job / groups;
+        const uint32_t j = (uint32_t)(job % groups) * 256 + threadIdx.x;
+        if (j >= a.n) continue;
         const uint32_t id = a.ids[t];
-        float y = a.base[at];
+        float y = a.base[t * a.n + j];
         if (id < a.n_adapters) {
             const uint32_t rank = rank_of(a, id);
-            if (rank) {
-                const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)j * a.max_rank * S;
-                const float* v = a.v + (size_t)t * a.v_stride;
-                float u = 0.0f;
-                for (uint32_t i = 0; i < rank; ++i) {
-                    uint32_t bits;
-                    if constexpr (S == 4) bits = *reinterpret_cast<const uint32_t*>(row + (size_t)i * 4);
-                    else bits = *reinterpret_cast<const uint16_t*>(row + (size_t)i * 2);
-                    u = fma_step(v[i], widen_bits<DT>(bits), u);
-                }
-                y = fma_step(a.scales ? a.scales[id] : 1.0f, u, y);
+            const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)j * a.max_rank * DtypeSize<DT>::value;
+            const float* v = a.v + t * a.v_stride;
+            float u = 0.0f;
+            for (uint32_t i0 = 0; i0 < rank; i0 += kGranule) {
+                float b[kGranule];
+                load_b<DT>(row, i0, a.max_rank, b);
+#pragma unroll
+                for (uint32_t i = 0; i < kGranule; ++i)
+                    if (i0 + i < rank) u = fma_step(v[i0 + i], b[i], u);
             }
+            if (rank) y = fma_step(scale_of(a, id), u, y);
         } else if (id != EIDM_NO_ADAPTER) {
             y = quiet_nan();
         }
-        a.out[at] = y;
+        a.out[t * a.n + j] = y;
+    }
+}
+
+// One wavefront per (16 rows, 64 columns).  v_mfma_f32_16x16x1_4b_f32, one
+// rank per step: all four blocks take the 16 rows of v, block s the columns
+// 4i+s, so a lane's results are four consecutive columns of four rows.
+template <int DT>
+__global__ __launch_bounds__(256) void expand_tile_kernel(LoraArgs a) {
+    const uint32_t lane = threadIdx.x & 63, i = lane & 15, s = lane >> 4;
+    const uint32_t groups = (a.n + 63) / 64;
+    const uint64_t tiles = ((uint64_t)a.m + 15) / 16;
+    for (uint64_t job = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < tiles * groups; job += (uint64_t)gridDim.x * 4) {
+        const uint64_t t0 = job / groups * 16;
+        const uint32_t j0 = (uint32_t)(job % groups) * 64 + 4 * i;  // this lane's output columns j0 .. j0+3
+        const uint64_t t = t0 + i < a.m ? t0 + i : a.m - 1;
+        const uint32_t mine = t0 + i < a.m ? a.ids[t] : EIDM_NO_ADAPTER;
+        f32x4 y[4];  // rows 4s .. 4s+3
+#pragma unroll
+        for (uint32_t v = 0; v < 4; ++v) {
+            const uint64_t r = t0 + 4 * s + v;
+            y[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (r < a.m) {
+                const float* p = a.base + r * a.n + j0;
+                if (j0 + 4 <= a.n) y[v] = *reinterpret_cast<const fr_f32x4_a4*>(p);
+                else
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c)
+                        if (j0 + c < a.n) y[v][c] = p[c];
+            }
+        }
+        for_each_adapter(mine, a.n_adapters, [&](uint32_t id, uint32_t members) {
+            const uint32_t rank = rank_of(a, id);
+            if (!rank) return;
+            const uint32_t col = min(j0 + s, a.n - 1);  // this lane's column of B
+            const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)col * a.max_rank * DtypeSize<DT>::value;
+            const float* v = a.v + t * a.v_stride;
+            f32x16 u{};
+            for (uint32_t i0 = 0; i0 < rank; i0 += kGranule) {
+                float b[kGranule];
+                load_b<DT>(row, i0, a.max_rank, b);
+                const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + i0), v1 = *reinterpret_cast<const f32x4*>(v + i0 + 4);
+#pragma unroll
+                for (uint32_t e = 0; e < kGranule; ++e)
+                    if (i0 + e < rank)  // wave-uniform
+                        u = __builtin_amdgcn_mfma_f32_16x16x1f32(e < 4 ? v0[e % 4] : v1[e % 4], b[e], u, 0, 0, 0);
+            }
+            const float scale = scale_of(a, id);
+#pragma unroll
+            for (uint32_t r = 0; r < 4; ++r)
+                if (members >> (4 * s + r) & 1)
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) y[r][c] = fma_step(scale, u[4 * c + r], y[r][c]);
+        });
+        const uint32_t bad = (uint32_t)__ballot(mine >= a.n_adapters && mine != EIDM_NO_ADAPTER) & 0xffffu;
+#pragma unroll
+        for (uint32_t v = 0; v < 4; ++v) {
+            const uint64_t r = t0 + 4 * s + v;
+            if (r >= a.m) continue;
+            if (bad >> (4 * s + v) & 1) y[v] = f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()};
+            float* p = a.out + r * a.n + j0;
+            if (j0 + 4 <= a.n) *reinterpret_cast<fr_f32x4_a4*>(p) = y[v];
+            else
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c)
+                    if (j0 + c < a.n) p[c] = y[v][c];
+        }
     }
 }
 
 uint32_t grid_of(uint64_t blocks, uint64_t most) { return (uint32_t)(blocks < most ? blocks : most); }
 
+// Rows of up to this many take the row forms.
+constexpr uint32_t kRowForm = 64;
+constexpr uint32_t kRowFormK = 16256;  // a staged row below 64 KB of LDS
+
 template <int DT>
 hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
-    const uint64_t jobs = (uint64_t)a.m * ((a.max_rank + 3) / 4);
+    if (a.m <= kRowForm && a.k <= kRowFormK) {
+        const uint32_t groups = (a.max_rank + 3) / 4;
+        const uint32_t waves = a.m * groups <= 1024 ? 1 : 4;
+        const uint32_t parts = (groups + waves - 1) / waves;
+        const uint32_t lds = few_row_floats(a.k) * 4;
+        hipLaunchKernelGGL(shrink_row_kernel<DT>, dim3(a.m * parts), dim3(64 * waves), lds, stream, a, parts);
+        return launched(EIDM_KERNEL_LORA_SHRINK, a.m * parts, 64 * waves, lds);
+    }
+    const uint64_t jobs = ((uint64_t)a.m + 15) / 16 * ((a.max_rank + 15) / 16);
     const uint32_t grid = grid_of((jobs + 3) / 4, (uint64_t)device_cus * 16);
-    hipLaunchKernelGGL(lora_shrink_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(shrink_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
     return launched(EIDM_KERNEL_LORA_SHRINK, grid, 256, 0);
 }
 
 template <int DT>
 hipError_t expand_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
-    const uint32_t grid = grid_of(((uint64_t)a.m * a.n + 255) / 256, (uint64_t)device_cus * 32);
-    hipLaunchKernelGGL(lora_expand_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
+    if (a.m <= kRowForm) {
+        const uint32_t grid = grid_of((uint64_t)a.m * ((a.n + 255) / 256), (uint64_t)device_cus * 32);
+        hipLaunchKernelGGL(expand_row_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
+        return launched(EIDM_KERNEL_LORA_EXPAND, grid, 256, 0);
+    }
+    const uint64_t jobs = ((uint64_t)a.m + 15) / 16 * ((a.n + 63) / 64);
+    const uint32_t grid = grid_of((jobs + 3) / 4, (uint64_t)device_cus * 64);
+    hipLaunchKernelGGL(expand_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
     return launched(EIDM_KERNEL_LORA_EXPAND, grid, 256, 0);
 }
 
