@@ -21,9 +21,10 @@ struct FewMap {
 
 __host__ __device__ constexpr uint32_t few_map_ids(uint32_t rows, uint32_t n_ids) { return n_ids < rows ? n_ids : rows; }
 
-// LDS words of a map of `rows` rows over n_ids ids
+// LDS words of a map of `rows` rows over n_ids ids, whole 16-byte units: what
+// follows is read 16 bytes at a time (off that boundary such a read is several)
 __host__ __device__ constexpr uint32_t few_map_words(uint32_t rows, uint32_t n_ids) {
-    return n_ids + 2 * few_map_ids(rows, n_ids) + 2 + rows;
+    return (n_ids + 2 * few_map_ids(rows, n_ids) + 2 + rows + 3) / 4 * 4;
 }
 
 __device__ __forceinline__ FewMap few_map_at(uint32_t* lds, uint32_t rows, uint32_t n_ids) {

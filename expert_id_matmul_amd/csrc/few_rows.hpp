@@ -38,23 +38,36 @@ constexpr int kFewRows = 16;  // activation rows of one pass over a weight row
 __host__ __device__ constexpr uint32_t few_row_floats(uint32_t k) { return (k + 127) / 128 * 128 + 16; }
 
 // Stages rows row_of(0 .. count-1) of k f32 elements (4-byte aligned) as LDS
-// rows 0 .. count-1; the whole block takes part.
+// rows 0 .. count-1; the whole block takes part, each thread with 8 loads in
+// flight (one at a time, a pass of 16 rows cost some 20 us of latency).
 template <typename RowOf>
 __device__ __forceinline__ void few_rows_stage(float* xs, uint32_t count, uint32_t k, RowOf row_of) {
+    constexpr uint32_t kBatch = 8;
     const uint32_t pieces = (k + 127) / 128 * 32;  // 16-byte pieces per row
     const uint32_t stride = few_row_floats(k);
-    for (uint32_t i = threadIdx.x; i < count * pieces; i += blockDim.x) {
-        const uint32_t r = i / pieces, p = i % pieces;
-        const float* src = row_of(r) + p * 4;
-        f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
-        if (p * 4 + 4 <= k) {
-            v = *reinterpret_cast<const fr_f32x4_a4*>(src);
-        } else {
+    const uint32_t total = count * pieces;
+    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kBatch * blockDim.x) {
+        f32x4 v[kBatch];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (p * 4 + j < k) v[j] = src[j];
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t i = i0 + j * blockDim.x, r = i / pieces, p = (i - r * pieces) * 4;
+            v[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (i >= total) continue;
+            const float* src = row_of(r) + p;
+            if (p + 4 <= k) {
+                v[j] = *reinterpret_cast<const fr_f32x4_a4*>(src);
+            } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 3; ++e)
+                    if (p + e < k) v[j][e] = src[e];
+            }
         }
-        *reinterpret_cast<f32x4*>(xs + (size_t)r * stride + (p / 32) * 128 + (p & 1) * 64 + (p % 32) / 2 * 4) = v;
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t i = i0 + j * blockDim.x, r = i / pieces, p = i - r * pieces;
+            if (i < total)
+                *reinterpret_cast<f32x4*>(xs + (size_t)r * stride + p / 32 * 128 + (p & 1) * 64 + p % 32 / 2 * 4) = v[j];
+        }
     }
 }
 

@@ -28,8 +28,10 @@ namespace eidm {
 namespace {
 
 constexpr int kWaves = 8;  // wavefronts per block
-// LDS for staged activation rows: one row of the longest k (kMaxDecodeRow)
-constexpr uint32_t kRowBytes = few_row_floats(kMaxDecodeRow) * 4;
+// LDS for staged activation rows: 16 rows of 2048, one of the longest k
+// (kMaxDecodeRow)
+constexpr uint32_t kRowBytes = 16 * few_row_floats(2048) * 4;
+static_assert(few_row_floats(kMaxDecodeRow) * 4 <= kRowBytes);
 constexpr uint32_t kRouteExperts = 256;  // experts a block routes itself (4 per lane)
 
 // most rows of k elements staged at once
@@ -246,7 +248,7 @@ hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream)
     static std::atomic<uint64_t> done[6];
     const uint32_t rows = a.m * a.top_k;
     const uint32_t touched = few_map_ids(rows, a.n_experts);  // at most
-    const uint32_t map_bytes = (few_map_words(rows, a.n_experts) + 3) / 4 * 16;
+    const uint32_t map_bytes = few_map_words(rows, a.n_experts) * 4;
     const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     auto blocks_of = [&](uint32_t groups) {
         const uint64_t jobs = (uint64_t)touched * groups;
