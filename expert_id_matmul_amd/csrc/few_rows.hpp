@@ -37,23 +37,38 @@ constexpr int kFewRows = 16;  // activation rows of one pass over a weight row
 // 16-byte read takes together fall on different banks.
 __host__ __device__ constexpr uint32_t few_row_floats(uint32_t k) { return (k + 127) / 128 * 128 + 16; }
 
-// Stages rows row_of(0 .. count-1) of k f32 elements (4-byte aligned) as LDS
-// rows 0 .. count-1; the whole block takes part, each thread with 8 loads in
-// flight (one at a time, a pass of 16 rows cost some 20 us of latency).
-template <typename RowOf>
-__device__ __forceinline__ void few_rows_stage(float* xs, uint32_t count, uint32_t k, RowOf row_of) {
-    constexpr uint32_t kBatch = 8;
-    const uint32_t pieces = (k + 127) / 128 * 32;  // 16-byte pieces per row
-    const uint32_t stride = few_row_floats(k);
-    const uint32_t total = count * pieces;
-    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kBatch * blockDim.x) {
-        f32x4 v[kBatch];
+// Copies rows row_of(0 .. count-1) of k f32 elements (4-byte aligned) to LDS
+// rows 0 .. count-1; the whole block takes part, each thread with kBatch loads
+// in flight.  issue() requests the first of them, finish() stores those and
+// copies the rest, so other work can stand between the two; a barrier must
+// follow before the rows are read.
+//
+// A wavefront takes units of 64 consecutive 16-byte pieces of one row, so
+// that all index arithmetic but a lane's own place is scalar (per thread it
+// was hoisted out of the caller's loops and spilled there).
+template <uint32_t kBatch, typename RowOf>
+struct FewStage {
+    float* xs;
+    uint32_t count, k;
+    RowOf row_of;
+    f32x4 v[kBatch];
+
+    __device__ __forceinline__ static uint32_t waves() { return blockDim.x >> 6; }
+    __device__ __forceinline__ static uint32_t wave() {
+        return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    }
+    __device__ __forceinline__ uint32_t pieces() const { return (k + 127) / 128 * 32; }  // of a row, zeros past k
+    __device__ __forceinline__ uint32_t units() const { return (pieces() + 63) / 64; }   // of a row
+
+    __device__ __forceinline__ void load(uint32_t u0) {
+        const uint32_t per = units();
 #pragma unroll
         for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t i = i0 + j * blockDim.x, r = i / pieces, p = (i - r * pieces) * 4;
-            v[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (i >= total) continue;
+            const uint32_t u = u0 + j * waves();
+            if (u >= count * per) break;  // wave-uniform
+            const uint32_t r = u / per, p = ((u - r * per) * 64 + (threadIdx.x & 63)) * 4;
             const float* src = row_of(r) + p;
+            v[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (p + 4 <= k) {
                 v[j] = *reinterpret_cast<const fr_f32x4_a4*>(src);
             } else {
@@ -62,13 +77,31 @@ __device__ __forceinline__ void few_rows_stage(float* xs, uint32_t count, uint32
                     if (p + e < k) v[j][e] = src[e];
             }
         }
+    }
+    __device__ __forceinline__ void store(uint32_t u0) const {
+        const uint32_t per = units(), stride = few_row_floats(k);
 #pragma unroll
         for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t i = i0 + j * blockDim.x, r = i / pieces, p = i - r * pieces;
-            if (i < total)
+            const uint32_t u = u0 + j * waves();
+            if (u >= count * per) break;
+            const uint32_t r = u / per, p = (u - r * per) * 64 + (threadIdx.x & 63);
+            if (p < pieces())
                 *reinterpret_cast<f32x4*>(xs + (size_t)r * stride + p / 32 * 128 + (p & 1) * 64 + p % 32 / 2 * 4) = v[j];
         }
     }
+    __device__ __forceinline__ void issue() { load(wave()); }
+    __device__ __forceinline__ void finish() {
+        store(wave());
+        for (uint32_t u0 = wave() + kBatch * waves(); u0 < count * units(); u0 += kBatch * waves()) {
+            load(u0);
+            store(u0);
+        }
+    }
+};
+
+template <uint32_t kBatch, typename RowOf>
+__device__ __forceinline__ FewStage<kBatch, RowOf> few_stage(float* xs, uint32_t count, uint32_t k, RowOf row_of) {
+    return FewStage<kBatch, RowOf>{xs, count, k, row_of, {}};
 }
 
 template <int DT>
@@ -85,81 +118,42 @@ __device__ __forceinline__ void few_widen(const fr_u32x4 (&p)[DtypeSize<DT>::val
     }
 }
 
-// Accumulates acc[g][c] over k.  RG row groups of four rows, xl[g] the LDS
-// row of this lane's row (row q of group g); RG = 0: one row, xl[0] in every
-// lane, and acc[0][c][0] of lane 4b+i is column i's slice sum; else
-// acc[g][c][v] of lane 4b+i is (row v, column i) of slice b.
-// wrow[c]: this lane's weight row (the caller repeats a valid one for lanes
-// that have none).  NT: weights are read once, by non-temporal loads.
-template <int DT, int C, int RG, int D, bool NT>
-__device__ __forceinline__ void few_rows_product(const uint8_t* const (&wrow)[C],
-                                                 const float* const (&xl)[RG ? RG : 1], int k,
-                                                 f32x4 (&acc)[RG ? RG : 1][C]) {
-    constexpr int S = DtypeSize<DT>::value;
-    constexpr int NP = S / 2;
-    constexpr int G = RG ? RG : 1;
-    const int b = (threadIdx.x & 63) >> 2;
-    const int full = k / kRoundK;
-
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[g][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
+// The weight stream of one wavefront: C weight rows per lane (4*C columns),
+// D rounds in flight.
+template <int DT, int C, int D, bool NT>
+struct FewStream {
+    static constexpr int S = DtypeSize<DT>::value;
+    static constexpr int NP = S / 2;
+    static constexpr int kColumns = C;
+    using Rows = const uint8_t* const (&)[C];
     struct Slot {
         fr_u32x4 w[C][NP];
     };
-    auto fetch = [&](int r, Slot& s) {
-        const size_t at = ((size_t)r * kRoundK + (size_t)b * kGranule) * S;
+    Slot ring[D];
+    Slot tail;  // the partial last round
+
+    __device__ __forceinline__ static int slice() { return (threadIdx.x & 63) >> 2; }
+
+    // wrow[c]: this lane's weight row (lanes without one repeat a valid row)
+    __device__ __forceinline__ static void fetch(const uint8_t* const (&wrow)[C], int r, Slot& s) {
+        const size_t at = ((size_t)r * kRoundK + (size_t)slice() * kGranule) * S;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at + 16 * i);
-                s.w[c][i] = NT ? __builtin_nontemporal_load(p) : *p;
+                s.w[c][i] = NT ? __builtin_nontemporal_load(p) : *p;  // NT: weights that are read once
             }
-    };
-    // four of a granule's products at a time: half the widened weights live
-    auto half = [&](int r, int h, const float (&w)[C][kGranule]) {
-        f32x4 x[G];
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            x[g] = *reinterpret_cast<const f32x4*>(xl[g] + r * kRoundK + h * 64 + b * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    if constexpr (RG == 0)
-                        acc[g][c][0] = fma_step(x[g][i], w[c][h * 4 + i], acc[g][c][0]);
-                    else
-                        acc[g][c] = mfma_step(x[g][i], w[c][h * 4 + i], acc[g][c]);
-                }
-    };
-    auto consume = [&](int r, const Slot& s) {
-        float w[C][kGranule];
-#pragma unroll
-        for (int c = 0; c < C; ++c) few_widen<DT>(s.w[c], w[c]);
-        half(r, 0, w);
-        half(r, 1, w);
-    };
-
-    Slot ring[D];
-    if (full > 0) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            fetch(min(d, full - 1), ring[d]);  // past the end: the last round again, never consumed
-            __builtin_amdgcn_sched_barrier(0);
-        }
     }
-    // the partial last round, requested behind the ring's first rounds
-    Slot tail{};
-    const int kk = full * kRoundK + b * kGranule;
-    if (kk < k) {
+
+    __device__ __forceinline__ void fetch_tail(const uint8_t* const (&wrow)[C], int k) {
+        const int full = k / kRoundK;
+        if (full * kRoundK == k) return;
+        const int kk = full * kRoundK + slice() * kGranule;
+        tail = Slot{};
         if (kk + kGranule <= k) {
-            fetch(full, tail);
-        } else {
+            fetch(wrow, full, tail);
+        } else if (kk < k) {  // a granule cut by k
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -173,25 +167,87 @@ __device__ __forceinline__ void few_rows_product(const uint8_t* const (&wrow)[C]
                     }
         }
     }
-    int r = 0;
-    for (; r + 2 * D <= full; r += D) {
+
+    // Requests the first rounds (and the partial one) of a product.
+    __device__ __forceinline__ void start(const uint8_t* const (&wrow)[C], int k) {
+        const int full = k / kRoundK;
+        if (full > 0) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            consume(r + d, ring[d]);
-            fetch(r + d + D, ring[d]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int d = 0; d < D; ++d) {
+                fetch(wrow, min(d, full - 1), ring[d]);  // past the end: the last round again, never consumed
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        fetch_tail(wrow, k);
+    }
+
+    // The product of the rows that start() requested; with MORE, start(next)
+    // has been done on return: its requests take the slots as the last rounds
+    // free them.  RG row groups of four activation rows in LDS, xl[g] this
+    // lane's row (row q of group g): acc[g][c][v] of lane 4b+i is (row v,
+    // column i) of slice b.  RG = 0: one row, the same in every lane, and
+    // acc[0][c][0] is column i's slice sum.
+    //
+    // Every slot is refilled unconditionally (past the end the last round is
+    // requested again), so that each wait counts the same loads on every path.
+    template <int RG, bool MORE>
+    __device__ __forceinline__ void run(Rows wrow, Rows next, const float* const (&xl)[RG ? RG : 1], int k,
+                                        f32x4 (&acc)[RG ? RG : 1][C]) {
+        constexpr int G = RG ? RG : 1;
+        const int b = slice();
+        const int full = k / kRoundK;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[g][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        auto consume = [&](int r, const Slot& s) {
+            float w[C][kGranule];
+#pragma unroll
+            for (int c = 0; c < C; ++c) few_widen<DT>(s.w[c], w[c]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4 x[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    x[g] = *reinterpret_cast<const f32x4*>(xl[g] + r * kRoundK + h * 64 + b * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            if constexpr (RG == 0)
+                                acc[g][c][0] = fma_step(x[g][i], w[c][h * 4 + i], acc[g][c][0]);
+                            else
+                                acc[g][c] = mfma_step(x[g][i], w[c][h * 4 + i], acc[g][c]);
+                        }
+            }
+        };
+
+        int r = 0;
+        for (; r + D < full; r += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                consume(r + d, ring[d]);
+                fetch(wrow, min(r + d + D, full - 1), ring[d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (full > 0) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (r + d < full) consume(r + d, ring[d]);
+                if constexpr (MORE) fetch(next, min(d, full - 1), ring[d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        if (full * kRoundK < k) {
+            consume(full, tail);
+            if constexpr (MORE) fetch_tail(next, k);
         }
     }
-#pragma unroll
-    for (int j = 0; j < 2 * D; ++j) {
-        if (r + j < full) {
-            consume(r + j, ring[j % D]);
-            if (r + j + D < full) fetch(r + j + D, ring[j % D]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    if (full * kRoundK < k) consume(full, tail);
-}
+};
 
 // The 16 slice sums of (row v, column i), v = 0..3, combined in the fixed
 // pairing by recursive halving: two of the four rows go to each half of the
@@ -216,38 +272,42 @@ __device__ __forceinline__ float few_rows_total(const f32x4& a) {
     return t;
 }
 
-// `count` (1..16) rows of LDS, rows[at .. at+count), times 4*C weight rows:
-// emit(row index, totals[C]) for every live row, in lanes that hold the
-// totals of column q = lane & 3 of each group.
-template <int DT, int C, int RG, int D, bool NT, typename Emit>
-__device__ __forceinline__ void few_rows_tile(const uint8_t* const (&wrow)[C], const float* xs, uint32_t stride,
-                                              uint32_t at, uint32_t count, int k, Emit emit) {
+// `count` (1..16) staged rows, row i at xs + lds_row(i) * stride, times the
+// 4*C weight rows that `w` has been started on (MORE: and is then started on
+// `next`): emit(i, totals[C]) for every
+// row, in lanes that hold the totals of column q = lane & 3 of each group.
+template <int RG, bool MORE, typename Stream, typename LdsRow, typename Emit>
+__device__ __forceinline__ void few_rows_tile(Stream& w, typename Stream::Rows wrow, typename Stream::Rows next,
+                                              const float* xs, uint32_t stride, uint32_t count, int k, LdsRow lds_row,
+                                              Emit emit) {
+    constexpr int C = Stream::kColumns;
     constexpr int G = RG ? RG : 1;
     const int lane = threadIdx.x & 63;
     const int b = lane >> 2;
     const uint32_t q = lane & 3;
     const float* xl[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) xl[g] = xs + (size_t)(at + (RG ? min(4 * g + q, count - 1) : 0)) * stride;
+    for (int g = 0; g < G; ++g) xl[g] = xs + (size_t)lds_row(RG ? min(4 * g + q, count - 1) : 0) * stride;
     f32x4 acc[G][C];
-    few_rows_product<DT, C, RG, D, NT>(wrow, xl, k, acc);
+    w.template run<RG, MORE>(wrow, next, xl, k, acc);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float v[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) v[c] = RG ? few_rows_total(acc[g][c]) : slice_tree(acc[g][c][0]);
         const uint32_t r = RG ? 4 * g + few_row(b) : 0;
-        if (RG ? ((b & 3) == 0 && r < count) : b == 0) emit(at + r, v);
+        if (RG ? ((b & 3) == 0 && r < count) : b == 0) emit(r, v);
     }
 }
 
-template <int DT, int C, int D, bool NT, typename Emit>
-__device__ __forceinline__ void few_rows_any(const uint8_t* const (&wrow)[C], const float* xs, uint32_t stride,
-                                             uint32_t at, uint32_t count, int k, Emit emit) {
-    if (count == 1) few_rows_tile<DT, C, 0, D, NT>(wrow, xs, stride, at, count, k, emit);
-    else if (count <= 4) few_rows_tile<DT, C, 1, D, NT>(wrow, xs, stride, at, count, k, emit);
-    else if (count <= 8) few_rows_tile<DT, C, 2, D, NT>(wrow, xs, stride, at, count, k, emit);
-    else few_rows_tile<DT, C, 4, D, NT>(wrow, xs, stride, at, count, k, emit);
+template <bool MORE, typename Stream, typename LdsRow, typename Emit>
+__device__ __forceinline__ void few_rows_any(Stream& w, typename Stream::Rows wrow, typename Stream::Rows next,
+                                             const float* xs, uint32_t stride, uint32_t count, int k, LdsRow lds_row,
+                                             Emit emit) {
+    if (count == 1) few_rows_tile<0, MORE>(w, wrow, next, xs, stride, count, k, lds_row, emit);
+    else if (count <= 4) few_rows_tile<1, MORE>(w, wrow, next, xs, stride, count, k, lds_row, emit);
+    else if (count <= 8) few_rows_tile<2, MORE>(w, wrow, next, xs, stride, count, k, lds_row, emit);
+    else few_rows_tile<4, MORE>(w, wrow, next, xs, stride, count, k, lds_row, emit);
 }
 
 }  // namespace eidm

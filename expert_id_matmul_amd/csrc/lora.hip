@@ -49,13 +49,16 @@ __global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t pa
     const uint32_t rank = rank_of(a, id);
     const uint32_t waves = blockDim.x >> 6;
     if (part * waves * 4 >= rank) return;
-    few_rows_stage(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
-    __syncthreads();
     const uint32_t i0 = (part * waves + (threadIdx.x >> 6)) * 4;
-    if (i0 >= rank) return;
     const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
                                     (size_t)min(i0 + q, rank - 1) * a.k * DtypeSize<DT>::value};
-    few_rows_tile<DT, 1, 0, 16, false>(wrow, xs, 0, 0, 1, (int)a.k, [&](uint32_t, const float (&v)[1]) {
+    FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 8 : 16, false> w;
+    w.start(wrow, (int)a.k);
+    auto stage = few_stage<8>(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
+    stage.issue();
+    stage.finish();
+    __syncthreads();
+    few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.k, [](uint32_t) { return 0; }, [&](uint32_t, const float (&v)[1]) {
         if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
     });
 }

@@ -27,7 +27,7 @@
 namespace eidm {
 namespace {
 
-constexpr int kWaves = 8;  // wavefronts per block
+constexpr int kWaves = 8;  // wavefronts per block of the many-token kernels
 // LDS for staged activation rows: 16 rows of 2048, one of the longest k
 // (kMaxDecodeRow)
 constexpr uint32_t kRowBytes = 16 * few_row_floats(2048) * 4;
@@ -37,37 +37,133 @@ constexpr uint32_t kRouteExperts = 256;  // experts a block routes itself (4 per
 // most rows of k elements staged at once
 __host__ __device__ constexpr uint32_t row_cap(uint32_t k) { return kRowBytes / (few_row_floats(k) * 4); }
 
-// Rounds in flight: 16 16-byte loads per lane.  (C weight rows per lane; one
-// load each for 16-bit weights, two for f32.)
+// Rounds in flight: `loads` 16-byte loads per lane (C weight rows per lane;
+// one load each for 16-bit weights, two for f32).
 template <int DT, int C>
-constexpr int few_depth() { return 32 / (C * DtypeSize<DT>::value); }
+constexpr int few_depth(int loads) {
+    return 2 * loads / (C * DtypeSize<DT>::value);
+}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
+// ------------------------------------------------------------ one token
+// A wavefront per slot; a block owns `cols` <= 4 columns of h for every slot
+// (so all compute units have the same share of each expert).  Routing as in
+// the fused decode step (moe_direct.hip): each expert's sigmoid by one
+// thread, every wavefront runs the selection up to its own pick, the last
+// one forms the gates.
+template <int DT, int NV, int MAXW>
+__global__ __launch_bounds__(64 * MAXW) void gate_up_one_kernel(MoeDecodeArgs a, uint32_t cols) {
+    constexpr int S = DtypeSize<DT>::value;
+    extern __shared__ __align__(16) float xs[];
+    __shared__ float rs_s[64 * NV];
+    __shared__ uint32_t rs_code[64 * NV];
+    const uint32_t lane = threadIdx.x & 63, slot = threadIdx.x >> 6, q = lane & 3;
+    RouteInputs<NV> rin;
+    route_inputs_issue<NV>(a.logits, a.bias, a.n_experts, rin);
+    __builtin_amdgcn_sched_barrier(0);  // the row's loads queue behind the router's
+    auto stage = few_stage<8>(xs, 1, a.hidden, [&](uint32_t) { return a.x; });
+    stage.issue();
+    __builtin_amdgcn_sched_barrier(0);
+    route_inputs_score<NV>(rin, a.n_experts, rs_s, rs_code);
+    stage.finish();
+    __syncthreads();
+
+    RouteScores<NV> sc;
+    route_scores_lds<NV>(rs_s, rs_code, sc);
+    uint32_t pick;
+    float score;
+    const float sum = route_select<NV>(sc, slot + 1, pick, score);
+    if (blockIdx.x == 0 && slot == a.top_k - 1 && lane < a.top_k) {
+        a.ids[lane] = pick;
+        a.gates[lane] = a.renormalize ? __fdiv_rn(score, sum) : score;
+    }
+    const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)pick, (int)slot);
+    const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.inter);
+    const uint32_t col = col0 + q;
+    const size_t at = (size_t)e * a.gate_up_stride + (size_t)(col < end ? col : col0) * a.hidden * S;
+    const uint8_t* const wrow[2] = {a.w_gate + at, a.w_up + at};
+    FewStream<DT, 2, few_depth<DT, 2>(MAXW > 8 ? 12 : 16), true> w;
+    w.start(wrow, (int)a.hidden);
+    few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.hidden, [](uint32_t) { return 0u; },
+                     [&](uint32_t, const float (&t)[2]) {
+                         if (col < end) a.h[(size_t)slot * a.inter + col] = silu_mul(t[0], t[1]);
+                     });
+}
+
+// A wavefront per slot; a block owns `cols` <= 8 output columns.
+template <int DT, int LOADS, int MAXW>
+__global__ __launch_bounds__(64 * MAXW) void down_one_kernel(MoeDecodeArgs a, uint32_t cols) {
+    constexpr int S = DtypeSize<DT>::value;
+    extern __shared__ __align__(16) float xs[];
+    __shared__ float ys[MAXW][8];
+    const uint32_t lane = threadIdx.x & 63, slot = threadIdx.x >> 6, q = lane & 3;
+    const uint32_t e = uniform(a.ids[slot]);
+    auto stage = few_stage<8>(xs, a.top_k, a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; });
+    stage.issue();
+    const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.hidden);
+    const uint8_t* wrow[2];
+#pragma unroll
+    for (uint32_t c = 0; c < 2; ++c) {
+        const uint32_t col = col0 + 4 * c + q;
+        wrow[c] = a.w_down + (size_t)e * a.down_stride + (size_t)(col < end ? col : col0) * a.inter * S;
+    }
+    FewStream<DT, 2, few_depth<DT, 2>(LOADS), true> w;
+    w.start(wrow, (int)a.inter);
+    stage.finish();
+    __syncthreads();
+    few_rows_tile<0, false>(w, wrow, wrow, xs, few_row_floats(a.inter), 1, (int)a.inter, [&](uint32_t) { return slot; },
+                     [&](uint32_t, const float (&t)[2]) {
+                         ys[slot][q] = t[0];
+                         ys[slot][4 + q] = t[1];
+                     });
+    __syncthreads();
+    if (slot == 0 && col0 + lane < end) {
+        float acc = 0.0f;
+        for (uint32_t s = 0; s < a.top_k; ++s) acc = __builtin_fmaf(a.gates[s], ys[s][lane], acc);
+        a.out[col0 + lane] = acc;
+    }
+}
+
+// --------------------------------------------------------- several tokens
+// Relative time of one column-group job for an expert of `rows` rows, `most`
+// of which are staged at once: the weights' stream alone for up to 4 rows,
+// the products beyond (measured at 16 rounds of k: 1, 2-4, 5-8 and 9-16 rows).
+__device__ __forceinline__ uint32_t job_cost(uint32_t rows, uint32_t most) {
+    auto pass = [](uint32_t r) { return r == 0 ? 0u : r <= 4 ? 8u : r <= 8 ? 10u : 15u; };
+    most = min(most, (uint32_t)kFewRows);
+    return rows / most * pass(most) + pass(rows % most);
+}
+
 // Column-group jobs (expert u, group g) of all touched experts in order, cut
-// into one contiguous range per block, so that a block meets one or two
-// experts: it stages their rows in LDS and its wavefronts take the range's
-// jobs in turn.  An expert whose rows do not fit takes several passes over
-// its weights.  row_of(routed row): the activation row of k elements.
+// into one contiguous range of equal cost per block, so that a block meets
+// one or two experts; its wavefronts take the range's jobs in turn, each
+// requesting its next job's weights while the last rounds of one run.
+// Rows: when `staged`, every row already stands in LDS, at lds_of(routed
+// row); else the block stages its experts' rows, in passes when they do not
+// fit.  row_of(routed row): the activation row of k elements.
 // weight_of(expert, group, wrow): this lane's weight rows.
 // emit(routed row, group, totals).
-template <int DT, int C, typename RowOf, typename WeightOf, typename Emit>
-__device__ __forceinline__ void expert_major(const FewMap& map, float* xs, uint32_t groups, uint32_t k, RowOf row_of,
-                                             WeightOf weight_of, Emit emit) {
-    const uint32_t jobs = *map.used * groups;
+template <int DT, int C, int D, typename RowOf, typename LdsOf, typename WeightOf, typename Emit>
+__device__ __forceinline__ void expert_major(const FewMap& map, float* xs, bool staged, uint32_t groups, uint32_t k,
+                                             RowOf row_of, LdsOf lds_of, WeightOf weight_of, Emit emit) {
     const uint32_t stride = few_row_floats(k);
     const uint32_t most = row_cap(k);
     const uint32_t per_expert = min(most, (uint32_t)kFewRows);
-    uint32_t pos = (uint32_t)((uint64_t)jobs * blockIdx.x / gridDim.x);
-    const uint32_t last = (uint32_t)((uint64_t)jobs * (blockIdx.x + 1) / gridDim.x);
+    const uint64_t cost = (uint64_t)map.cost[*map.used] * groups;
+    uint32_t pos = few_map_job(map, groups, cost * blockIdx.x / gridDim.x);
+    const uint32_t last = few_map_job(map, groups, cost * (blockIdx.x + 1) / gridDim.x);
     while (pos < last) {  // block-uniform
         uint32_t v = pos / groups;  // experts pos/groups .. v in this pass
         const uint32_t first = map.off[v];
         uint32_t end = map.off[v + 1];
         uint32_t passes = 1;
-        if (end - first > per_expert) {
+        if (staged) {
+            v = (last - 1) / groups;
+            end = map.off[v + 1];
+        } else if (end - first > per_expert) {
             passes = (end - first + per_expert - 1) / per_expert;
         } else {
             while ((v + 1) * groups < last && map.off[v + 2] - end <= per_expert && map.off[v + 2] - first <= most) {
@@ -79,18 +175,46 @@ __device__ __forceinline__ void expert_major(const FewMap& map, float* xs, uint3
         for (uint32_t p = 0; p < passes; ++p) {
             const uint32_t base = first + p * per_expert;
             const uint32_t limit = passes == 1 ? end : min(end, base + per_expert);
-            __syncthreads();  // the rows of the pass before are done with
-            few_rows_stage(xs, limit - base, k, [&](uint32_t i) { return row_of(map.row[base + i]); });
-            __syncthreads();
-            for (uint32_t job = pos + (threadIdx.x >> 6); job < stop; job += kWaves) {
+            FewStream<DT, C, D, true> w;
+            const uint8_t* wrow[C];
+            auto weights_at = [&](uint32_t job, const uint8_t* (&to)[C]) {
                 const uint32_t u = uniform(job / groups);
-                const uint32_t g = uniform(job) - u * groups;
-                const uint32_t from = max(uniform(map.off[u]), base), to = min(uniform(map.off[u + 1]), limit);
-                const uint8_t* wrow[C];
-                weight_of(uniform(map.id[u]), g, wrow);
-                few_rows_any<DT, C, few_depth<DT, C>(), true>(
-                    wrow, xs, stride, from - base, to - from, (int)k,
-                    [&](uint32_t i, const float (&t)[C]) { emit(map.row[base + i], g, t); });
+                weight_of(uniform(map.id[u]), uniform(job) - u * groups, to);
+            };
+            uint32_t job = pos + (threadIdx.x >> 6);
+            if (job < stop) {
+                weights_at(job, wrow);
+                w.start(wrow, (int)k);
+            }
+            if (!staged) {
+                __syncthreads();  // the rows of the pass before are done with
+                auto stage = few_stage<8>(xs, limit - base, k, [&](uint32_t i) { return row_of(map.row[base + i]); });
+                stage.issue();
+                stage.finish();
+                __syncthreads();
+            }
+            while (job < stop) {  // wave-uniform
+                const uint32_t u = uniform(job / groups), g = uniform(job) - u * groups;
+                const uint32_t to = min(uniform(map.off[u + 1]), limit);
+                for (uint32_t at = max(uniform(map.off[u]), base); at < to; at += kFewRows) {
+                    // (one turn unless an expert's staged rows exceed 16)
+                    const bool again = at + kFewRows < to;
+                    const uint32_t count = min(to - at, (uint32_t)kFewRows);
+                    auto lds_row = [&](uint32_t i) { return staged ? lds_of(map.row[at + i]) : at + i - base; };
+                    auto emit_at = [&](uint32_t i, const float (&t)[C]) { emit(map.row[at + i], g, t); };
+                    const uint8_t* next[C];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) next[c] = wrow[c];
+                    if (again || job + kWaves < stop) {
+                        if (!again) weights_at(job + kWaves, next);
+                        few_rows_any<true>(w, wrow, next, xs, stride, count, (int)k, lds_row, emit_at);
+#pragma unroll
+                        for (int c = 0; c < C; ++c) wrow[c] = next[c];
+                    } else {
+                        few_rows_any<false>(w, wrow, next, xs, stride, count, (int)k, lds_row, emit_at);
+                    }
+                }
+                job += kWaves;
             }
         }
         pos = stop;
@@ -103,34 +227,44 @@ template <int DT, bool ROUTE>
 __global__ __launch_bounds__(64 * kWaves) void gate_up_kernel(MoeDecodeArgs a) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) uint32_t lds[];
+    __shared__ uint32_t picks[ROUTE ? kWaves * kMaxDecodeTopK : 1];
     const uint32_t rows = a.m * a.top_k;
     const FewMap map = few_map_at(lds, rows, a.n_experts);
     float* xs = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));
+    const bool staged = a.m <= row_cap(a.hidden);  // every token's row fits
+    auto stage = few_stage<8>(xs, staged ? a.m : 0, a.hidden, [&](uint32_t t) { return a.x + (size_t)t * a.hidden; });
+    const uint32_t* ids = a.ids;
     if constexpr (ROUTE) {
-        __shared__ uint32_t picks[kWaves * kMaxDecodeTopK];
         const uint32_t t = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        RouteScores<kRouteExperts / 64> sc;
+        if (t < a.m) route_scores<kRouteExperts / 64>(a.logits + (size_t)t * a.n_experts, a.bias, a.n_experts, sc);
+        stage.issue();
         if (t < a.m) {
             uint32_t id;
-            float gate;
-            route_token<kRouteExperts / 64>(a.logits + (size_t)t * a.n_experts, a.bias, a.n_experts, a.top_k,
-                                            a.renormalize, id, gate);
+            float score;
+            const float sum = route_select<kRouteExperts / 64>(sc, a.top_k, id, score);
             if (lane < a.top_k) {
                 picks[t * a.top_k + lane] = id;
                 if (blockIdx.x == 0) {
                     a.ids[t * a.top_k + lane] = id;
-                    a.gates[t * a.top_k + lane] = gate;
+                    a.gates[t * a.top_k + lane] = a.renormalize ? __fdiv_rn(score, sum) : score;
                 }
             }
         }
+        ids = picks;
         __syncthreads();
-        few_map_build(map, picks, rows, a.n_experts, a.m);
     } else {
-        few_map_build(map, a.ids, rows, a.n_experts, a.m);
+        stage.issue();
     }
+    const uint32_t most = row_cap(a.hidden);
+    few_map_build(map, ids, rows, a.n_experts, [&](uint32_t r) { return job_cost(r, most); });
+    stage.finish();
+    __syncthreads();
 
     const uint32_t q = threadIdx.x & 3;
-    expert_major<DT, 2>(
-        map, xs, (a.inter + 3) / 4, a.hidden, [&](uint32_t r) { return a.x + (size_t)(r / a.top_k) * a.hidden; },
+    expert_major<DT, 2, few_depth<DT, 2>(12)>(
+        map, xs, staged, (a.inter + 3) / 4, a.hidden, [&](uint32_t r) { return a.x + (size_t)(r / a.top_k) * a.hidden; },
+        [&](uint32_t r) { return r / a.top_k; },
         [&](uint32_t e, uint32_t g, const uint8_t* (&wrow)[2]) {
             const size_t at = (size_t)e * a.gate_up_stride + (size_t)min(g * 4 + q, a.inter - 1) * a.hidden * S;
             wrow[0] = a.w_gate + at;
@@ -142,17 +276,19 @@ __global__ __launch_bounds__(64 * kWaves) void gate_up_kernel(MoeDecodeArgs a) {
 }
 
 // y[r] = W_down[e] h[r], 4*C columns per job
-template <int DT, int C>
+template <int DT, int C, int LOADS>
 __global__ __launch_bounds__(64 * kWaves) void down_kernel(MoeDecodeArgs a) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) uint32_t lds[];
     const uint32_t rows = a.m * a.top_k;
     const FewMap map = few_map_at(lds, rows, a.n_experts);
     float* xs = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));
-    few_map_build(map, a.ids, rows, a.n_experts, a.m);
+    const uint32_t most = row_cap(a.inter);
+    few_map_build(map, a.ids, rows, a.n_experts, [&](uint32_t r) { return job_cost(r, most); });
     const uint32_t q = threadIdx.x & 3;
-    expert_major<DT, C>(
-        map, xs, (a.hidden + 4 * C - 1) / (4 * C), a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; },
+    expert_major<DT, C, few_depth<DT, C>(LOADS)>(
+        map, xs, false, (a.hidden + 4 * C - 1) / (4 * C), a.inter,
+        [&](uint32_t r) { return a.h + (size_t)r * a.inter; }, [](uint32_t) { return 0u; },
         [&](uint32_t e, uint32_t g, const uint8_t* (&wrow)[C]) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -168,55 +304,75 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(MoeDecodeArgs a) {
         });
 }
 
-// Few rows: all of h staged; a block owns `cols` <= 4*C output columns of
+// Few rows: all of h staged; a block owns `cols` <= 8 output columns of
 // every token, its wavefronts take the touched experts in turn.
-template <int DT, int C>
+template <int DT, int LOADS>
 __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs a, uint32_t cols) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) uint32_t lds[];
     const uint32_t rows = a.m * a.top_k;
     const FewMap map = few_map_at(lds, rows, a.n_experts);
-    float* ys = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));  // [rows][4*C]
-    float* xs = ys + rows * 4 * C;
-    few_map_build(map, a.ids, rows, a.n_experts, a.m);
-    few_rows_stage(xs, rows, a.inter, [&](uint32_t i) { return a.h + (size_t)map.row[i] * a.inter; });
-    __syncthreads();
+    float* ys = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));  // [rows][8]
+    float* xs = ys + rows * 8;
+    auto stage = few_stage<8>(xs, rows, a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; });
+    stage.issue();
+    few_map_build(map, a.ids, rows, a.n_experts, [](uint32_t) { return 1u; });
 
     const uint32_t q = threadIdx.x & 3;
-    const uint32_t col0 = blockIdx.x * cols;
+    const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.hidden);
     const uint32_t used = *map.used;
-    for (uint32_t w = threadIdx.x >> 6; w < used; w += kWaves) {
-        const uint32_t u = uniform(w);
-        const uint32_t from = uniform(map.off[u]), to = uniform(map.off[u + 1]);
-        const uint8_t* wrow[C];
+    auto weights_at = [&](uint32_t u, const uint8_t* (&to)[2]) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const uint32_t col = 4 * c + q < cols ? min(col0 + 4 * c + q, a.hidden - 1) : col0;
-            wrow[c] = a.w_down + (size_t)uniform(map.id[u]) * a.down_stride + (size_t)col * a.inter * S;
+        for (uint32_t c = 0; c < 2; ++c) {
+            const uint32_t col = col0 + 4 * c + q;
+            to[c] = a.w_down + (size_t)uniform(map.id[u]) * a.down_stride + (size_t)(col < end ? col : col0) * a.inter * S;
         }
-        for (uint32_t at = from; at < to; at += kFewRows)
-            few_rows_any<DT, C, few_depth<DT, C>(), true>(
-                wrow, xs, few_row_floats(a.inter), at, min(to - at, (uint32_t)kFewRows), (int)a.inter,
-                [&](uint32_t i, const float (&t)[C]) {
-#pragma unroll
-                    for (int c = 0; c < C; ++c) ys[map.row[i] * (4 * C) + 4 * c + q] = t[c];
-                });
+    };
+    FewStream<DT, 2, few_depth<DT, 2>(LOADS), true> w;
+    const uint8_t* wrow[2];
+    uint32_t u = uniform(threadIdx.x >> 6);
+    if (u < used) {
+        weights_at(u, wrow);
+        w.start(wrow, (int)a.inter);
+    }
+    stage.finish();
+    __syncthreads();
+    for (; u < used; u += kWaves) {
+        const uint32_t to = uniform(map.off[u + 1]);
+        for (uint32_t at = uniform(map.off[u]); at < to; at += kFewRows) {
+            const bool again = at + kFewRows < to;
+            const uint32_t count = min(to - at, (uint32_t)kFewRows), stride = few_row_floats(a.inter);
+            auto lds_row = [&](uint32_t i) { return map.row[at + i]; };
+            auto emit = [&](uint32_t i, const float (&t)[2]) {
+                ys[map.row[at + i] * 8 + q] = t[0];
+                ys[map.row[at + i] * 8 + 4 + q] = t[1];
+            };
+            const uint8_t* next[2] = {wrow[0], wrow[1]};
+            if (again || u + kWaves < used) {
+                if (!again) weights_at(u + kWaves, next);
+                few_rows_any<true>(w, wrow, next, xs, stride, count, (int)a.inter, lds_row, emit);
+                wrow[0] = next[0];
+                wrow[1] = next[1];
+            } else {
+                few_rows_any<false>(w, wrow, next, xs, stride, count, (int)a.inter, lds_row, emit);
+            }
+        }
     }
     __syncthreads();
-    const uint32_t live = min(cols, a.hidden - col0);
-    for (uint32_t i = threadIdx.x; i < a.m * 4 * C; i += blockDim.x) {
-        const uint32_t t = i / (4 * C), c = i % (4 * C);
-        if (c < live) {
+    for (uint32_t i = threadIdx.x; i < a.m * 8; i += blockDim.x) {
+        const uint32_t t = i / 8, c = i % 8;
+        if (col0 + c < end) {
             float acc = 0.0f;
             for (uint32_t s = 0; s < a.top_k; ++s) {
                 const uint32_t r = t * a.top_k + s;
-                acc = __builtin_fmaf(a.gates[r], ys[r * (4 * C) + c], acc);
+                acc = __builtin_fmaf(a.gates[r], ys[r * 8 + c], acc);
             }
             a.out[(size_t)t * a.hidden + col0 + c] = acc;
         }
     }
 }
 
+// ---------------------------------------------------------------- launches
 // Allows a kernel the whole LDS of a compute unit, once per device.
 hipError_t allow_lds(const void* kernel, std::atomic<uint64_t>& done) {
     int dev = 0;
@@ -224,56 +380,98 @@ hipError_t allow_lds(const void* kernel, std::atomic<uint64_t>& done) {
     if (err != hipSuccess) return err;
     const uint64_t bit = 1ull << (dev & 63);
     if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024 - 1024);
+    err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 156 * 1024);
     if (err == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return err;
 }
 
-template <typename Kernel, typename... Args>
-hipError_t launch_one(int receipt, Kernel kernel, std::atomic<uint64_t>& done, uint32_t grid, uint32_t lds,
-                      hipStream_t stream, Args... args) {
-    if (lds > 64 * 1024) {
-        const hipError_t err = allow_lds(reinterpret_cast<const void*>(kernel), done);
+template <auto Kernel, typename... Args>
+hipError_t launch_one(int receipt, uint32_t grid, uint32_t threads, uint32_t lds, hipStream_t stream, Args... args) {
+    if (lds > 48 * 1024) {
+        static std::atomic<uint64_t> done{0};
+        const hipError_t err = allow_lds(reinterpret_cast<const void*>(Kernel), done);
         if (err != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * kWaves), lds, stream, args...);
-    return launched(receipt, grid, 64 * kWaves, lds);
+    hipLaunchKernelGGL(Kernel, dim3(grid), dim3(threads), lds, stream, args...);
+    return launched(receipt, grid, threads, lds);
 }
 
-// Every row of h fits in LDS beside the map and the output rows
-bool combine_in_down(const MoeDecodeArgs& a) { return a.m * a.top_k <= row_cap(a.inter); }
+// Columns per block in [most/2, most]: the width whose blocks, spread over
+// the compute units, give the busiest one the fewest columns; the widest on
+// ties.
+uint32_t block_columns(uint32_t n, uint32_t most, uint32_t cus) {
+    uint32_t best = most;
+    uint64_t least = ~0ull;
+    for (uint32_t c = most; c >= (most + 1) / 2; --c) {
+        const uint64_t blocks = (n + c - 1) / c, cost = (blocks + cus - 1) / cus * c;
+        if (cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
+}
+
+// 12 loads in flight where they hold the whole product, or cut it into whole
+// rings where 16 do not; else 16.
+bool twelve_loads(int dtype, uint32_t k, uint32_t weight_rows) {
+    const uint32_t rounds = k / kRoundK, per = weight_rows * (dtype == kDtypeF32 ? 2 : 1);
+    return rounds <= 12 / per || (rounds % (16 / per) && rounds % (12 / per) == 0);
+}
+
+template <int DT>
+hipError_t launch_one_token(const MoeDecodeArgs& a, uint32_t cus, hipStream_t stream) {
+    const uint32_t threads = 64 * a.top_k;
+    const uint32_t up = block_columns(a.inter, 4, cus), down = block_columns(a.hidden, 8, cus);
+    const uint32_t up_blocks = (a.inter + up - 1) / up, down_blocks = (a.hidden + down - 1) / down;
+    const uint32_t up_lds = few_row_floats(a.hidden) * 4, down_lds = a.top_k * few_row_floats(a.inter) * 4;
+    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN;
+    const bool wide = a.top_k > 8;
+    hipError_t err;
+    if (a.n_experts <= 256)
+        err = wide ? launch_one<gate_up_one_kernel<DT, 4, 16>>(U, up_blocks, threads, up_lds, stream, a, up)
+                   : launch_one<gate_up_one_kernel<DT, 4, 8>>(U, up_blocks, threads, up_lds, stream, a, up);
+    else
+        err = wide ? launch_one<gate_up_one_kernel<DT, 32, 16>>(U, up_blocks, threads, up_lds, stream, a, up)
+                   : launch_one<gate_up_one_kernel<DT, 32, 8>>(U, up_blocks, threads, up_lds, stream, a, up);
+    if (err != hipSuccess) return err;
+    if (wide) return launch_one<down_one_kernel<DT, 12, 16>>(W, down_blocks, threads, down_lds, stream, a, down);
+    return twelve_loads(DT, a.inter, 2)
+               ? launch_one<down_one_kernel<DT, 12, 8>>(W, down_blocks, threads, down_lds, stream, a, down)
+               : launch_one<down_one_kernel<DT, 16, 8>>(W, down_blocks, threads, down_lds, stream, a, down);
+}
 
 template <int DT>
 hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream) {
-    static std::atomic<uint64_t> done[6];
+    const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     const uint32_t rows = a.m * a.top_k;
+    if (a.m == 1 && a.top_k <= row_cap(a.inter)) return launch_one_token<DT>(a, cus, stream);
     const uint32_t touched = few_map_ids(rows, a.n_experts);  // at most
     const uint32_t map_bytes = few_map_words(rows, a.n_experts) * 4;
-    const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     auto blocks_of = [&](uint32_t groups) {
         const uint64_t jobs = (uint64_t)touched * groups;
         return (uint32_t)(jobs < cus ? jobs : cus);
     };
-    auto staged = [&](uint32_t k) { return (rows < row_cap(k) ? rows : row_cap(k)) * few_row_floats(k) * 4; };
+    auto staged = [&](uint32_t count, uint32_t k) { return (count < row_cap(k) ? count : row_cap(k)) * few_row_floats(k) * 4; };
+    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN;
+    constexpr uint32_t threads = 64 * kWaves;
     const bool route = a.m <= (uint32_t)kWaves && a.n_experts <= kRouteExperts;
     hipError_t err = hipSuccess;
     if (!route) {
         err = launch_route(a.logits, a.bias, a.m, a.n_experts, a.top_k, a.renormalize, a.ids, a.gates, stream);
         if (err != hipSuccess) return err;
     }
-    const uint32_t up_blocks = blocks_of((a.inter + 3) / 4), up_lds = map_bytes + staged(a.hidden);
-    err = route ? launch_one(EIDM_KERNEL_DECODE_GATE_UP, gate_up_kernel<DT, true>, done[0], up_blocks, up_lds, stream, a)
-                : launch_one(EIDM_KERNEL_DECODE_GATE_UP, gate_up_kernel<DT, false>, done[1], up_blocks, up_lds, stream, a);
+    const uint32_t up_blocks = blocks_of((a.inter + 3) / 4), up_lds = map_bytes + staged(rows, a.hidden);
+    err = route ? launch_one<gate_up_kernel<DT, true>>(U, up_blocks, threads, up_lds, stream, a)
+                : launch_one<gate_up_kernel<DT, false>>(U, up_blocks, threads, up_lds, stream, a);
     if (err != hipSuccess) return err;
-    if (combine_in_down(a)) {
-        const uint32_t cols = a.hidden >= 8 * cus ? 8 : 4;
-        const uint32_t blocks = (a.hidden + cols - 1) / cols;
-        const uint32_t lds = map_bytes + rows * cols * 4 + staged(a.inter);
-        return cols == 8 ? launch_one(EIDM_KERNEL_DECODE_DOWN, down_combine_kernel<DT, 2>, done[2], blocks, lds, stream, a, cols)
-                         : launch_one(EIDM_KERNEL_DECODE_DOWN, down_combine_kernel<DT, 1>, done[3], blocks, lds, stream, a, cols);
+    if (rows <= row_cap(a.inter)) {  // every row of h fits beside the map and the output rows
+        const uint32_t cols = block_columns(a.hidden, 8, cus), blocks = (a.hidden + cols - 1) / cols;
+        const uint32_t lds = map_bytes + rows * 32 + staged(rows, a.inter);
+        return launch_one<down_combine_kernel<DT, 12>>(W, blocks, threads, lds, stream, a, cols);
     }
-    err = launch_one(EIDM_KERNEL_DECODE_DOWN, down_kernel<DT, 4>, done[4], blocks_of((a.hidden + 15) / 16),
-                     map_bytes + staged(a.inter), stream, a);
+    const uint32_t blocks = blocks_of((a.hidden + 7) / 8), lds = map_bytes + staged(rows, a.inter);
+    err = launch_one<down_kernel<DT, 2, 12>>(W, blocks, threads, lds, stream, a);
     if (err != hipSuccess) return err;
     return launch_combine(a.m, a.top_k, a.hidden, a.y, a.gates, a.out, stream);
 }
