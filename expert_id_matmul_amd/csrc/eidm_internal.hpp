@@ -139,6 +139,10 @@ struct LoraArgs {
     uint32_t* zero_ids;  // [m] ids of the shared projection, written by the shrink (or null)
 };
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream);
+// out = W x for a few rows (any alignment), and the shrink of those rows
+bool lora_base_few_supported(const LoraArgs& a);
+hipError_t launch_lora_base_few(const LoraArgs& a, int weight_dtype, const uint8_t* weights, int device_cus,
+                                hipStream_t stream);
 hipError_t launch_lora_expand(const LoraArgs& a, int device_cus, hipStream_t stream);
 // a.ids is ignored: the kernel writes the picks to `ids` and reads them itself
 hipError_t launch_moe_direct(const MatmulArgs& a, const float* logits, const float* bias, int renormalize,

@@ -12,7 +12,8 @@
 // adapter.  By tiles (prompts, where neighbouring rows share an adapter):
 // a wavefront takes 16 consecutive rows and runs once over each adapter that
 // occurs among them, so no row needs sorting and all rows are read and
-// written in their order.
+// written in their order.  A decode batch's shared projection and its shrink
+// run side by side in one launch.
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
@@ -35,32 +36,82 @@ __device__ __forceinline__ void write_zero_ids(const LoraArgs& a) {
             a.zero_ids[i] = 0;
 }
 
-// One block per row and blockDim/64 groups of four ranks; the row is staged
-// in LDS.
+// Work of one block of 256: ranks 16*part .. of row t, four per wavefront;
+// the row is staged in LDS.
 template <int DT>
-__global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t parts) {
-    extern __shared__ __align__(16) float xs[];
-    const int lane = threadIdx.x & 63;
-    const uint32_t q = lane & 3;
-    write_zero_ids(a);
-    const uint32_t t = blockIdx.x / parts, part = blockIdx.x % parts;
+__device__ __forceinline__ void shrink_row(const LoraArgs& a, uint32_t t, uint32_t part, float* xs) {
+    const uint32_t q = threadIdx.x & 3;
     const uint32_t id = a.ids[t];
     if (id >= a.n_adapters) return;
     const uint32_t rank = rank_of(a, id);
-    const uint32_t waves = blockDim.x >> 6;
-    if (part * waves * 4 >= rank) return;
-    const uint32_t i0 = (part * waves + (threadIdx.x >> 6)) * 4;
+    if (part * 16 >= rank) return;
+    const uint32_t i0 = part * 16 + (threadIdx.x >> 6) * 4;
     const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
                                     (size_t)min(i0 + q, rank - 1) * a.k * DtypeSize<DT>::value};
     FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 8 : 16, false> w;
-    w.start(wrow, (int)a.k);
+    if (i0 < rank) w.start(wrow, (int)a.k);  // wave-uniform
     auto stage = few_stage<8>(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
     stage.issue();
     stage.finish();
     __syncthreads();
-    few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.k, [](uint32_t) { return 0; }, [&](uint32_t, const float (&v)[1]) {
-        if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
-    });
+    if (i0 >= rank) return;
+    few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.k, [](uint32_t) { return 0; },
+                            [&](uint32_t, const float (&v)[1]) {
+                                if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
+                            });
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t parts) {
+    extern __shared__ __align__(16) float xs[];
+    write_zero_ids(a);
+    shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, xs);
+}
+
+// The shared projection of up to 64 rows (a.out = W x) and, in the first
+// `shrinks` blocks of the same launch, the shrink of those rows, which needs
+// none of it.  RG 0, 1 (one row, up to four): rows staged in LDS, each
+// wavefront four columns; else RT = -RG row tiles of 16 rows against 16
+// columns per block.
+template <int DT, int RG>
+__global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t* weights, uint32_t shrinks,
+                                                       uint32_t parts) {
+    extern __shared__ __align__(16) float xs[];
+    if (blockIdx.x < shrinks) {
+        shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, xs);
+        return;
+    }
+    const uint32_t block = blockIdx.x - shrinks, lane = threadIdx.x & 63;
+    if constexpr (RG >= 0) {
+        const uint32_t q = lane & 3, col = block * 16 + (threadIdx.x >> 6) * 4 + q;
+        const bool live = col - q < a.n;  // wave-uniform
+        const uint8_t* const wrow[1] = {weights + (size_t)min(col, a.n - 1) * a.k * DtypeSize<DT>::value};
+        FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 8 : 16, true> w;
+        if (live) w.start(wrow, (int)a.k);
+        auto stage = few_stage<8>(xs, a.m, a.k, [&](uint32_t t) { return a.x + (size_t)t * a.k; });
+        stage.issue();
+        stage.finish();
+        __syncthreads();
+        if (!live) return;
+        few_rows_tile<RG, false>(w, wrow, wrow, xs, few_row_floats(a.k), a.m, (int)a.k, [](uint32_t i) { return i; },
+                                 [&](uint32_t t, const float (&v)[1]) {
+                                     if (col < a.n) a.out[(size_t)t * a.n + col] = v[0];
+                                 });
+    } else {
+        constexpr int RT = -RG;
+        const uint32_t i = lane & 15, col = block * 16 + i;
+        const float* xrow[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(t * 16 + i, a.m - 1) * a.k;
+        float total[RT];
+        rows16_product<DT, RT, RT >= 4 ? 4 : 8, true>(weights + (size_t)min(col, a.n - 1) * a.k * DtypeSize<DT>::value,
+                                                      xrow, (int)a.k, xs, total);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const uint32_t r = t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
+            if (r < a.m && col < a.n) a.out[(size_t)r * a.n + col] = total[t];
+        }
+    }
 }
 
 // A tile of 16 consecutive rows: lane l holds row l%16's adapter (`none` for
@@ -77,30 +128,29 @@ __device__ __forceinline__ void for_each_adapter(uint32_t mine, uint32_t n_adapt
     }
 }
 
-// One wavefront per (16 rows, 16 ranks).
+// One block per (16 rows, 16 ranks).
 template <int DT>
 __global__ __launch_bounds__(256) void shrink_tile_kernel(LoraArgs a) {
+    __shared__ __align__(16) float xs[rows16_lds(1)];
     const uint32_t lane = threadIdx.x & 63, i = lane & 15;
     const uint32_t chunks = (a.max_rank + 15) / 16;
     const uint64_t tiles = ((uint64_t)a.m + 15) / 16;
     write_zero_ids(a);
-    for (uint64_t job = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < tiles * chunks; job += (uint64_t)gridDim.x * 4) {
+    for (uint64_t job = blockIdx.x; job < tiles * chunks; job += gridDim.x) {
         const uint64_t t0 = job / chunks * 16;
         const uint32_t c0 = (uint32_t)(job % chunks) * 16;
         const uint64_t t = t0 + i < a.m ? t0 + i : a.m - 1;
         const uint32_t mine = t0 + i < a.m ? a.ids[t] : EIDM_NO_ADAPTER;
         for_each_adapter(mine, a.n_adapters, [&](uint32_t id, uint32_t members) {
             const uint32_t rank = rank_of(a, id);
-            if (c0 >= rank) return;
-            const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
-                                            (size_t)min(c0 + i, rank - 1) * a.k * DtypeSize<DT>::value};
-            f32x4 total[1];
-            rows16_product<DT, 1, 8, false>(wrow, a.x + t * a.k, (int)a.k, total);
-#pragma unroll
-            for (uint32_t v = 0; v < 4; ++v) {
-                const uint32_t r = 4 * (lane >> 4) + v;
-                if ((members >> r & 1) && c0 + i < rank) a.v[(t0 + r) * a.v_stride + c0 + i] = total[0][v];
-            }
+            if (c0 >= rank) return;  // block-uniform
+            const float* const xrow[1] = {a.x + t * a.k};
+            float total[1];
+            rows16_product<DT, 1, 8, false>(a.a + (size_t)id * a.a_stride +
+                                                (size_t)min(c0 + i, rank - 1) * a.k * DtypeSize<DT>::value,
+                                            xrow, (int)a.k, xs, total);
+            const uint32_t r = 4 * (lane >> 4) + (threadIdx.x >> 6);
+            if ((members >> r & 1) && c0 + i < rank) a.v[(t0 + r) * a.v_stride + c0 + i] = total[0];
         });
     }
 }
@@ -119,9 +169,10 @@ __device__ __forceinline__ void load_b(const uint8_t* row, uint32_t i0, uint32_t
     }
 }
 
-// One thread per output: the row's adapter alone.
+// One thread per output: the row's adapter alone, 32 ranks' loads at once.
 template <int DT>
 __global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
+    constexpr uint32_t kBatch = 4;
     const uint32_t groups = (a.n + 255) / 256;
     for (uint64_t job = blockIdx.x; job < (uint64_t)a.m * groups; job += gridDim.x) {
         const uint64_t t = job / groups;
@@ -134,12 +185,16 @@ __global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
             const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)j * a.max_rank * DtypeSize<DT>::value;
             const float* v = a.v + t * a.v_stride;
             float u = 0.0f;
-            for (uint32_t i0 = 0; i0 < rank; i0 += kGranule) {
-                float b[kGranule];
-                load_b<DT>(row, i0, a.max_rank, b);
+            for (uint32_t i0 = 0; i0 < rank; i0 += kBatch * kGranule) {
+                float b[kBatch][kGranule];
 #pragma unroll
-                for (uint32_t i = 0; i < kGranule; ++i)
-                    if (i0 + i < rank) u = fma_step(v[i0 + i], b[i], u);
+                for (uint32_t h = 0; h < kBatch; ++h)
+                    if (i0 + h * kGranule < rank) load_b<DT>(row, i0 + h * kGranule, a.max_rank, b[h]);
+#pragma unroll
+                for (uint32_t h = 0; h < kBatch; ++h)
+#pragma unroll
+                    for (uint32_t i = 0; i < kGranule; ++i)
+                        if (i0 + h * kGranule + i < rank) u = fma_step(v[i0 + h * kGranule + i], b[h][i], u);
             }
             if (rank) y = fma_step(scale_of(a, id), u, y);
         } else if (id != EIDM_NO_ADAPTER) {
@@ -218,23 +273,43 @@ __global__ __launch_bounds__(256) void expand_tile_kernel(LoraArgs a) {
 uint32_t grid_of(uint64_t blocks, uint64_t most) { return (uint32_t)(blocks < most ? blocks : most); }
 
 // Rows of up to this many take the row forms.
-constexpr uint32_t kRowForm = 64;
-constexpr uint32_t kRowFormK = 16256;  // a staged row below 64 KB of LDS
+constexpr uint32_t kRowForm = EIDM_DECODE_MAX_TOKENS;
+constexpr uint32_t kRowLds = 64 * 1024;  // LDS of staged rows
+
+bool stages_rows(uint32_t rows, uint32_t k) { return (uint64_t)rows * few_row_floats(k) * 4 <= kRowLds; }
 
 template <int DT>
 hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
-    if (a.m <= kRowForm && a.k <= kRowFormK) {
-        const uint32_t groups = (a.max_rank + 3) / 4;
-        const uint32_t waves = a.m * groups <= 1024 ? 1 : 4;
-        const uint32_t parts = (groups + waves - 1) / waves;
-        const uint32_t lds = few_row_floats(a.k) * 4;
-        hipLaunchKernelGGL(shrink_row_kernel<DT>, dim3(a.m * parts), dim3(64 * waves), lds, stream, a, parts);
-        return launched(EIDM_KERNEL_LORA_SHRINK, a.m * parts, 64 * waves, lds);
+    if (a.m <= kRowForm && stages_rows(1, a.k)) {
+        const uint32_t parts = (a.max_rank + 15) / 16, lds = few_row_floats(a.k) * 4;
+        hipLaunchKernelGGL(shrink_row_kernel<DT>, dim3(a.m * parts), dim3(256), lds, stream, a, parts);
+        return launched(EIDM_KERNEL_LORA_SHRINK, a.m * parts, 256, lds);
     }
     const uint64_t jobs = ((uint64_t)a.m + 15) / 16 * ((a.max_rank + 15) / 16);
-    const uint32_t grid = grid_of((jobs + 3) / 4, (uint64_t)device_cus * 16);
+    const uint32_t grid = grid_of(jobs, (uint64_t)device_cus * 16);
     hipLaunchKernelGGL(shrink_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
     return launched(EIDM_KERNEL_LORA_SHRINK, grid, 256, 0);
+}
+
+template <int DT, int RG>
+hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
+    const uint32_t parts = (a.max_rank + 15) / 16, shrinks = with_shrink ? a.m * parts : 0;
+    const uint32_t blocks = (a.n + 15) / 16;
+    uint32_t lds = RG >= 0 ? a.m * few_row_floats(a.k) * 4 : rows16_lds(-RG) * 4;
+    if (with_shrink && lds < few_row_floats(a.k) * 4) lds = few_row_floats(a.k) * 4;
+    hipLaunchKernelGGL((base_few_kernel<DT, RG>), dim3(shrinks + blocks), dim3(256), lds, stream, a, weights, shrinks,
+                       parts);
+    return launched(EIDM_KERNEL_LORA_BASE, shrinks + blocks, 256, lds);
+}
+
+template <int DT>
+hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
+    if (a.m <= 4 && stages_rows(a.m, a.k))
+        return a.m == 1 ? base_few<DT, 0>(a, weights, with_shrink, stream)
+                        : base_few<DT, 1>(a, weights, with_shrink, stream);
+    if (a.m <= 16) return base_few<DT, -1>(a, weights, with_shrink, stream);
+    if (a.m <= 32) return base_few<DT, -2>(a, weights, with_shrink, stream);
+    return base_few<DT, -4>(a, weights, with_shrink, stream);
 }
 
 template <int DT>
@@ -257,6 +332,23 @@ hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t str
     case kDtypeF32: return shrink_dt<kDtypeF32>(a, device_cus, stream);
     case kDtypeF16: return shrink_dt<kDtypeF16>(a, device_cus, stream);
     case kDtypeBF16: return shrink_dt<kDtypeBF16>(a, device_cus, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+bool lora_base_few_supported(const LoraArgs& a) { return a.m <= kRowForm; }
+
+hipError_t launch_lora_base_few(const LoraArgs& a, int weight_dtype, const uint8_t* weights, int device_cus,
+                                hipStream_t stream) {
+    const bool together = weight_dtype == a.dtype && stages_rows(1, a.k);
+    if (!together) {
+        const hipError_t err = launch_lora_shrink(a, device_cus, stream);
+        if (err != hipSuccess) return err;
+    }
+    switch (weight_dtype) {
+    case kDtypeF32: return base_few_dt<kDtypeF32>(a, weights, together, stream);
+    case kDtypeF16: return base_few_dt<kDtypeF16>(a, weights, together, stream);
+    case kDtypeBF16: return base_few_dt<kDtypeBF16>(a, weights, together, stream);
     default: return hipErrorInvalidValue;
     }
 }
@@ -418,14 +510,21 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
     a.base = weights ? output : base;
     a.v = reinterpret_cast<float*>(ws);
     a.out = output;
-    a.zero_ids = weights ? reinterpret_cast<uint32_t*>(ws + z.off_ids) : nullptr;
-    hipError_t err = eidm::launch_lora_shrink(a, eidm::device_cus(), st);
-    if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter shrink launch: %s", hipGetErrorString(err));
-    if (weights) {
-        const eidm_shape s = eidm::shared_projection(shape);
-        rc = eidm_matmul_id(&s, EIDM_ROUTE_AUTO, weights, weight_bytes, input, a.zero_ids, output, ws + z.off_matmul,
-                            z.matmul, stream, nullptr);
-        if (rc) return rc;
+    hipError_t err;
+    if (weights && shape->arith == EIDM_ARITH_F32 && eidm::lora_base_few_supported(a)) {
+        err = eidm::launch_lora_base_few(a, shape->weight_dtype, static_cast<const uint8_t*>(weights),
+                                         eidm::device_cus(), st);
+        if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "projection launch: %s", hipGetErrorString(err));
+    } else {
+        if (weights) a.zero_ids = reinterpret_cast<uint32_t*>(ws + z.off_ids);
+        err = eidm::launch_lora_shrink(a, eidm::device_cus(), st);
+        if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter shrink launch: %s", hipGetErrorString(err));
+        if (weights) {
+            const eidm_shape s = eidm::shared_projection(shape);
+            rc = eidm_matmul_id(&s, EIDM_ROUTE_AUTO, weights, weight_bytes, input, a.zero_ids, output,
+                                ws + z.off_matmul, z.matmul, stream, nullptr);
+            if (rc) return rc;
+        }
     }
     err = eidm::launch_lora_expand(a, eidm::device_cus(), st);
     if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter expand launch: %s", hipGetErrorString(err));
