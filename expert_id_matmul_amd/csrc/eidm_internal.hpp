@@ -137,10 +137,17 @@ struct LoraArgs {
     const float *scales, *x, *base;
     float *v, *out;
     uint32_t* zero_ids;  // [m] ids of the shared projection, written by the shrink (or null)
+    // the id -> row map of the rows (null: the row forms)
+    const uint32_t *counts, *offsets, *rows;
+    uint32_t* tiles;  // the sorted rows in tiles of 16, written by the shrink
 };
+// rows up to which each reads its adapter by itself at any rank; more are
+// sorted by adapter when rows times ranks make that the faster form
+constexpr uint32_t kLoraRowForm = 64;
+bool lora_sorts_rows(uint32_t m, uint32_t k, uint32_t max_rank);
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream);
-// out = W x for a few rows (any alignment), and the shrink of those rows
-bool lora_base_few_supported(const LoraArgs& a);
+// out = W x for up to some hundred rows (any alignment), and the shrink of them
+bool lora_base_few_supported(const LoraArgs& a, int device_cus);
 hipError_t launch_lora_base_few(const LoraArgs& a, int weight_dtype, const uint8_t* weights, int device_cus,
                                 hipStream_t stream);
 hipError_t launch_lora_expand(const LoraArgs& a, int device_cus, hipStream_t stream);

@@ -201,16 +201,41 @@ struct FewStream {
 #pragma unroll
             for (int c = 0; c < C; ++c) acc[g][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+        // the activations of a round (both halves of this lane's granule); with
+        // at most four rows they are read one round ahead, since then a
+        // wavefront's few steps do not cover the latency of an LDS read
+        constexpr bool kAhead = RG <= 1;
+        f32x4 ahead[G][2];
+        auto read = [&](int r, int h, f32x4 (&x)[G]) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) x[g] = *reinterpret_cast<const f32x4*>(xl[g] + r * kRoundK + h * 64 + b * 4);
+        };
+        auto read_ahead = [&](int r) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32x4 x[G];
+                read(r, h, x);
+#pragma unroll
+                for (int g = 0; g < G; ++g) ahead[g][h] = x[g];
+            }
+        };
+        const int last = (k + kRoundK - 1) / kRoundK - 1;
+        if constexpr (kAhead) read_ahead(0);
         auto consume = [&](int r, const Slot& s) {
+            f32x4 x[2][G];
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) x[h][g] = ahead[g][h];
+                read_ahead(min(r + 1, last));
+            }
             float w[C][kGranule];
 #pragma unroll
             for (int c = 0; c < C; ++c) few_widen<DT>(s.w[c], w[c]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                f32x4 x[G];
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    x[g] = *reinterpret_cast<const f32x4*>(xl[g] + r * kRoundK + h * 64 + b * 4);
+                if constexpr (!kAhead) read(r, h, x[h]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -218,9 +243,9 @@ struct FewStream {
 #pragma unroll
                         for (int c = 0; c < C; ++c) {
                             if constexpr (RG == 0)
-                                acc[g][c][0] = fma_step(x[g][i], w[c][h * 4 + i], acc[g][c][0]);
+                                acc[g][c][0] = fma_step(x[h][g][i], w[c][h * 4 + i], acc[g][c][0]);
                             else
-                                acc[g][c] = mfma_step(x[g][i], w[c][h * 4 + i], acc[g][c]);
+                                acc[g][c] = mfma_step(x[h][g][i], w[c][h * 4 + i], acc[g][c]);
                         }
             }
         };

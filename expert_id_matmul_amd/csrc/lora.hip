@@ -9,14 +9,14 @@
 //
 // Two forms of each, with the same bits.  By rows (a decode batch, where
 // rows have adapters of their own): a wavefront takes one row and streams its
-// adapter.  By tiles (prompts, where neighbouring rows share an adapter):
-// a wavefront takes 16 consecutive rows and runs once over each adapter that
-// occurs among them, so no row needs sorting and all rows are read and
-// written in their order.  A decode batch's shared projection and its shrink
+// adapter.  By tiles (prompts, where many rows share an adapter): the rows are
+// sorted by adapter (the library's id -> row map) and 16 rows of one adapter
+// read it once.  A decode batch's shared projection and its shrink
 // run side by side in one launch.
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
+#include "few_map.hpp"
 #include "few_rows.hpp"
 #include "rows16.hpp"
 
@@ -48,10 +48,10 @@ __device__ __forceinline__ void shrink_row(const LoraArgs& a, uint32_t t, uint32
     const uint32_t i0 = part * 16 + (threadIdx.x >> 6) * 4;
     const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
                                     (size_t)min(i0 + q, rank - 1) * a.k * DtypeSize<DT>::value};
-    FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 8 : 16, false> w;
-    if (i0 < rank) w.start(wrow, (int)a.k);  // wave-uniform
+    FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 4 : 8, false> w;
     auto stage = few_stage<8>(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
-    stage.issue();
+    stage.issue();  // ahead of the weights: a thread's loads return in order
+    w.start(wrow, (int)a.k);  // in every wavefront: behind a branch, the rows' wait would be for the weights too
     stage.finish();
     __syncthreads();
     if (i0 >= rank) return;
@@ -68,28 +68,26 @@ __global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t pa
     shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, xs);
 }
 
-// The shared projection of up to 64 rows (a.out = W x) and, in the first
-// `shrinks` blocks of the same launch, the shrink of those rows, which needs
-// none of it.  RG 0, 1 (one row, up to four): rows staged in LDS, each
-// wavefront four columns; else RT = -RG row tiles of 16 rows against 16
-// columns per block.
+// The shared projection (a.out = W x) and, in the last `shrinks` blocks of
+// the same launch, the row form's shrink, which needs none of it.  RG 0, 1 (one row, up to four): rows staged in LDS, each
+// wavefront four columns; else blocks of 16*T rows by 16*T columns, T = -RG.
 template <int DT, int RG>
 __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t* weights, uint32_t shrinks,
                                                        uint32_t parts) {
     extern __shared__ __align__(16) float xs[];
-    if (blockIdx.x < shrinks) {
-        shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, xs);
+    const uint32_t block = blockIdx.x, bases = gridDim.x - shrinks, lane = threadIdx.x & 63;
+    if (block >= bases) {
+        shrink_row<DT>(a, (block - bases) / parts, (block - bases) % parts, xs);
         return;
     }
-    const uint32_t block = blockIdx.x - shrinks, lane = threadIdx.x & 63;
     if constexpr (RG >= 0) {
         const uint32_t q = lane & 3, col = block * 16 + (threadIdx.x >> 6) * 4 + q;
         const bool live = col - q < a.n;  // wave-uniform
         const uint8_t* const wrow[1] = {weights + (size_t)min(col, a.n - 1) * a.k * DtypeSize<DT>::value};
-        FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 8 : 16, true> w;
-        if (live) w.start(wrow, (int)a.k);
+        FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 4 : 8, true> w;
         auto stage = few_stage<8>(xs, a.m, a.k, [&](uint32_t t) { return a.x + (size_t)t * a.k; });
         stage.issue();
+        w.start(wrow, (int)a.k);
         stage.finish();
         __syncthreads();
         if (!live) return;
@@ -98,61 +96,82 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
                                      if (col < a.n) a.out[(size_t)t * a.n + col] = v[0];
                                  });
     } else {
-        constexpr int RT = -RG;
-        const uint32_t i = lane & 15, col = block * 16 + i;
-        const float* xrow[RT];
+        // block (column tile, row tile), the row tiles of one column tile on
+        // one XCD, whose L2 then serves the weights to all but the first
+        constexpr int T = -RG;
+        const uint32_t rtiles = (a.m + 16 * T - 1) / (16 * T), i = lane & 15;
+        const uint32_t group = block / (8 * rtiles), in = block % (8 * rtiles);
+        const uint32_t col0 = (group * 8 + in % 8) * 16 * T, row0 = in / 8 * 16 * T;
+        if (col0 >= a.n) return;  // the last group of column tiles
+        const uint8_t* wrow[T];
+        const float* xrow[T];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(t * 16 + i, a.m - 1) * a.k;
-        float total[RT];
-        rows16_product<DT, RT, RT >= 4 ? 4 : 8, true>(weights + (size_t)min(col, a.n - 1) * a.k * DtypeSize<DT>::value,
-                                                      xrow, (int)a.k, xs, total);
+        for (int t = 0; t < T; ++t) {
+            wrow[t] = weights + (size_t)min(col0 + t * 16 + i, a.n - 1) * a.k * DtypeSize<DT>::value;
+            xrow[t] = a.x + (size_t)min(row0 + t * 16 + i, a.m - 1) * a.k;
+        }
+        float total[T][T];
+        rows16_product<DT, T, T, T == 1 ? 8 : 4, false>(wrow, xrow, (int)a.k, xs, total);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const uint32_t r = t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
-            if (r < a.m && col < a.n) a.out[(size_t)r * a.n + col] = total[t];
+        for (int t = 0; t < T; ++t) {
+            const uint32_t r = row0 + t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
+#pragma unroll
+            for (int c = 0; c < T; ++c)
+                if (r < a.m && col0 + c * 16 + i < a.n) a.out[(size_t)r * a.n + col0 + c * 16 + i] = total[t][c];
         }
     }
 }
 
-// A tile of 16 consecutive rows: lane l holds row l%16's adapter (`none` for
-// a row past the last).  Calls body(id, members) for every adapter id <
-// n_adapters among them, members a bit per row of the tile.
-template <typename Body>
-__device__ __forceinline__ void for_each_adapter(uint32_t mine, uint32_t n_adapters, Body body) {
-    uint32_t left = (uint32_t)__ballot(mine < n_adapters) & 0xffffu;
-    while (left) {  // wave-uniform
-        const uint32_t id = (uint32_t)__builtin_amdgcn_readlane((int)mine, __builtin_ctz(left));
-        const uint32_t members = (uint32_t)__ballot(mine == id) & 0xffffu;
-        left &= ~members;
-        body(id, members);
+// The sorted rows in tiles: 16 rows of one adapter each (fewer in an adapter's
+// last).  Adapter a's tiles start at slot offsets[a] / 16 + a, which leaves
+// room for every partial tile before it without counting them; a slot behind
+// an adapter's last tile is empty.  Id n_adapters: the rows without an adapter.
+struct Tile {
+    uint32_t id, at, count;  // adapter, first sorted row, rows (0: empty slot)
+};
+
+__device__ __forceinline__ Tile tile_of(const LoraArgs& a, uint32_t slot) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t before = 0;  // ids whose first slot is at or before this one
+    for (uint32_t i0 = 0; i0 <= a.n_adapters; i0 += 64) {
+        const uint32_t i = min(i0 + lane, a.n_adapters);
+        before += (uint32_t)__popcll(__ballot(i0 + lane <= a.n_adapters && a.offsets[i] / 16 + i <= slot));
     }
+    const uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane((int)before) - 1;  // id 0 starts at slot 0
+    const uint32_t begin = a.offsets[id], end = a.offsets[id + 1];
+    const uint32_t at = begin + (slot - (begin / 16 + id)) * 16;
+    return {id, at, at < end ? min(end - at, 16u) : 0u};
 }
 
-// One block per (16 rows, 16 ranks).
+// A tile as the shrink leaves it for the expand: id << 5 | count, then the 16
+// rows (the last one repeated) from word 4 on.
+constexpr uint32_t kTileWords = 20;
+
+// One block per (slot, 16 ranks).
 template <int DT>
-__global__ __launch_bounds__(256) void shrink_tile_kernel(LoraArgs a) {
+__global__ __launch_bounds__(256, DT == kDtypeF32 ? 3 : 4) void shrink_tile_kernel(LoraArgs a, uint32_t chunks) {
     __shared__ __align__(16) float xs[rows16_lds(1)];
     const uint32_t lane = threadIdx.x & 63, i = lane & 15;
-    const uint32_t chunks = (a.max_rank + 15) / 16;
-    const uint64_t tiles = ((uint64_t)a.m + 15) / 16;
     write_zero_ids(a);
-    for (uint64_t job = blockIdx.x; job < tiles * chunks; job += gridDim.x) {
-        const uint64_t t0 = job / chunks * 16;
-        const uint32_t c0 = (uint32_t)(job % chunks) * 16;
-        const uint64_t t = t0 + i < a.m ? t0 + i : a.m - 1;
-        const uint32_t mine = t0 + i < a.m ? a.ids[t] : EIDM_NO_ADAPTER;
-        for_each_adapter(mine, a.n_adapters, [&](uint32_t id, uint32_t members) {
-            const uint32_t rank = rank_of(a, id);
-            if (c0 >= rank) return;  // block-uniform
-            const float* const xrow[1] = {a.x + t * a.k};
-            float total[1];
-            rows16_product<DT, 1, 8, false>(a.a + (size_t)id * a.a_stride +
-                                                (size_t)min(c0 + i, rank - 1) * a.k * DtypeSize<DT>::value,
-                                            xrow, (int)a.k, xs, total);
-            const uint32_t r = 4 * (lane >> 4) + (threadIdx.x >> 6);
-            if ((members >> r & 1) && c0 + i < rank) a.v[(t0 + r) * a.v_stride + c0 + i] = total[0];
-        });
+    const uint32_t slot = blockIdx.x / chunks, c0 = blockIdx.x % chunks * 16;
+    const Tile t = tile_of(a, slot);
+    const uint32_t row = t.count ? a.rows[t.at + min(i, t.count - 1)] : 0;
+    if (c0 == 0 && threadIdx.x < 16) {
+        uint32_t* entry = a.tiles + (size_t)slot * kTileWords;
+        if (i == 0) entry[0] = t.id << 5 | t.count;
+        entry[4 + i] = row;
     }
+    if (!t.count || t.id == a.n_adapters) return;  // block-uniform
+    const uint32_t rank = rank_of(a, t.id);
+    if (c0 >= rank) return;
+    const float* const xrow[1] = {a.x + (size_t)row * a.k};
+    const uint8_t* const wrow[1] = {a.a + (size_t)t.id * a.a_stride +
+                                    (size_t)min(c0 + i, rank - 1) * a.k * DtypeSize<DT>::value};
+    float total[1][1];
+    rows16_product<DT, 1, 1, 6, false>(wrow, xrow, (int)a.k, xs, total);
+    const uint32_t r = 4 * (lane >> 4) + (threadIdx.x >> 6);
+    const uint32_t to = (uint32_t)__shfl((int)row, (int)r);
+    if (r < t.count && c0 + i < rank) a.v[(size_t)to * a.v_stride + c0 + i] = total[0][0];
 }
 
 // Ranks i0 .. i0+7 of one row of B, widened; those past max_rank are not read.
@@ -204,98 +223,97 @@ __global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
     }
 }
 
-// One wavefront per (16 rows, 64 columns).  v_mfma_f32_16x16x1_4b_f32, one
-// rank per step: all four blocks take the 16 rows of v, block s the columns
-// 4i+s, so a lane's results are four consecutive columns of four rows.
+// One block per (slot, 256 columns), 64 columns per wavefront.
+// v_mfma_f32_16x16x1_4b_f32, one rank per step: all four blocks take the 16
+// rows of v, block s the columns 4i+s, so a lane's results are four
+// consecutive columns of four rows.  The base rows dominate: their addresses
+// wait for the tile's entry alone.
 template <int DT>
-__global__ __launch_bounds__(256) void expand_tile_kernel(LoraArgs a) {
+__global__ __launch_bounds__(256) void expand_tile_kernel(LoraArgs a, uint32_t parts) {
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, s = lane >> 4;
-    const uint32_t groups = (a.n + 63) / 64;
-    const uint64_t tiles = ((uint64_t)a.m + 15) / 16;
-    for (uint64_t job = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); job < tiles * groups; job += (uint64_t)gridDim.x * 4) {
-        const uint64_t t0 = job / groups * 16;
-        const uint32_t j0 = (uint32_t)(job % groups) * 64 + 4 * i;  // this lane's output columns j0 .. j0+3
-        const uint64_t t = t0 + i < a.m ? t0 + i : a.m - 1;
-        const uint32_t mine = t0 + i < a.m ? a.ids[t] : EIDM_NO_ADAPTER;
-        f32x4 y[4];  // rows 4s .. 4s+3
+    const uint32_t* entry = a.tiles + (size_t)(blockIdx.x / parts) * kTileWords;
+    const uint32_t j0 = (blockIdx.x % parts * 4 + (threadIdx.x >> 6)) * 64 + 4 * i;  // this lane's columns j0 .. j0+3
+    const uint32_t id = entry[0] >> 5, count = entry[0] & 31;
+    if (!count || j0 - 4 * i >= a.n) return;  // wave-uniform
+    uint32_t row[4];  // this lane's rows 4s .. 4s+3
 #pragma unroll
-        for (uint32_t v = 0; v < 4; ++v) {
-            const uint64_t r = t0 + 4 * s + v;
-            y[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < a.m) {
-                const float* p = a.base + r * a.n + j0;
-                if (j0 + 4 <= a.n) y[v] = *reinterpret_cast<const fr_f32x4_a4*>(p);
-                else
+    for (uint32_t v = 0; v < 4; ++v) row[v] = entry[4 + 4 * s + v];
+    const float* v_row = a.v + (size_t)entry[4 + i] * a.v_stride;
+    f32x4 y[4];
 #pragma unroll
-                    for (uint32_t c = 0; c < 4; ++c)
-                        if (j0 + c < a.n) y[v][c] = p[c];
-            }
+    for (uint32_t v = 0; v < 4; ++v) {
+        const float* p = a.base + (size_t)row[v] * a.n + j0;
+        if (j0 + 4 <= a.n) y[v] = *reinterpret_cast<const fr_f32x4_a4*>(p);
+        else
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) y[v][c] = j0 + c < a.n ? p[c] : 0.0f;
+    }
+    if (id < a.n_adapters) {  // wave-uniform
+        const uint32_t rank = rank_of(a, id);
+        const uint32_t col = min(j0 + s, a.n - 1);  // this lane's column of B
+        const uint8_t* b_row = a.b + (size_t)id * a.b_stride + (size_t)col * a.max_rank * DtypeSize<DT>::value;
+        f32x16 u{};
+        for (uint32_t i0 = 0; i0 < rank; i0 += kGranule) {
+            float b[kGranule];
+            load_b<DT>(b_row, i0, a.max_rank, b);
+            const f32x4 v0 = *reinterpret_cast<const f32x4*>(v_row + i0);
+            const f32x4 v1 = *reinterpret_cast<const f32x4*>(v_row + i0 + 4);
+#pragma unroll
+            for (uint32_t e = 0; e < kGranule; ++e)
+                if (i0 + e < rank)  // wave-uniform
+                    u = __builtin_amdgcn_mfma_f32_16x16x1f32(e < 4 ? v0[e % 4] : v1[e % 4], b[e], u, 0, 0, 0);
         }
-        for_each_adapter(mine, a.n_adapters, [&](uint32_t id, uint32_t members) {
-            const uint32_t rank = rank_of(a, id);
-            if (!rank) return;
-            const uint32_t col = min(j0 + s, a.n - 1);  // this lane's column of B
-            const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)col * a.max_rank * DtypeSize<DT>::value;
-            const float* v = a.v + t * a.v_stride;
-            f32x16 u{};
-            for (uint32_t i0 = 0; i0 < rank; i0 += kGranule) {
-                float b[kGranule];
-                load_b<DT>(row, i0, a.max_rank, b);
-                const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + i0), v1 = *reinterpret_cast<const f32x4*>(v + i0 + 4);
-#pragma unroll
-                for (uint32_t e = 0; e < kGranule; ++e)
-                    if (i0 + e < rank)  // wave-uniform
-                        u = __builtin_amdgcn_mfma_f32_16x16x1f32(e < 4 ? v0[e % 4] : v1[e % 4], b[e], u, 0, 0, 0);
-            }
+        if (rank) {
             const float scale = scale_of(a, id);
 #pragma unroll
             for (uint32_t r = 0; r < 4; ++r)
-                if (members >> (4 * s + r) & 1)
 #pragma unroll
-                    for (uint32_t c = 0; c < 4; ++c) y[r][c] = fma_step(scale, u[4 * c + r], y[r][c]);
-        });
-        const uint32_t bad = (uint32_t)__ballot(mine >= a.n_adapters && mine != EIDM_NO_ADAPTER) & 0xffffu;
-#pragma unroll
-        for (uint32_t v = 0; v < 4; ++v) {
-            const uint64_t r = t0 + 4 * s + v;
-            if (r >= a.m) continue;
-            if (bad >> (4 * s + v) & 1) y[v] = f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()};
-            float* p = a.out + r * a.n + j0;
-            if (j0 + 4 <= a.n) *reinterpret_cast<fr_f32x4_a4*>(p) = y[v];
-            else
-#pragma unroll
-                for (uint32_t c = 0; c < 4; ++c)
-                    if (j0 + c < a.n) p[c] = y[v][c];
+                for (uint32_t c = 0; c < 4; ++c) y[r][c] = fma_step(scale, u[4 * c + r], y[r][c]);
         }
+    }
+#pragma unroll
+    for (uint32_t v = 0; v < 4; ++v) {
+        if (4 * s + v >= count) continue;
+        if (id == a.n_adapters && a.ids[row[v]] != EIDM_NO_ADAPTER)
+            y[v] = f32x4{quiet_nan(), quiet_nan(), quiet_nan(), quiet_nan()};
+        float* p = a.out + (size_t)row[v] * a.n + j0;
+        if (j0 + 4 <= a.n) *reinterpret_cast<fr_f32x4_a4*>(p) = y[v];
+        else
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c)
+                if (j0 + c < a.n) p[c] = y[v][c];
     }
 }
 
+// Slots of the tiles of m sorted rows.
+uint64_t lora_slots(uint32_t m, uint32_t n_adapters) { return (uint64_t)m / 16 + n_adapters + 1; }
+
 uint32_t grid_of(uint64_t blocks, uint64_t most) { return (uint32_t)(blocks < most ? blocks : most); }
 
-// Rows of up to this many take the row forms.
-constexpr uint32_t kRowForm = EIDM_DECODE_MAX_TOKENS;
 constexpr uint32_t kRowLds = 64 * 1024;  // LDS of staged rows
 
 bool stages_rows(uint32_t rows, uint32_t k) { return (uint64_t)rows * few_row_floats(k) * 4 <= kRowLds; }
 
 template <int DT>
 hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
-    if (a.m <= kRowForm && stages_rows(1, a.k)) {
-        const uint32_t parts = (a.max_rank + 15) / 16, lds = few_row_floats(a.k) * 4;
+    const uint32_t parts = (a.max_rank + 15) / 16;
+    if (!a.rows) {
+        const uint32_t lds = few_row_floats(a.k) * 4;
         hipLaunchKernelGGL(shrink_row_kernel<DT>, dim3(a.m * parts), dim3(256), lds, stream, a, parts);
         return launched(EIDM_KERNEL_LORA_SHRINK, a.m * parts, 256, lds);
     }
-    const uint64_t jobs = ((uint64_t)a.m + 15) / 16 * ((a.max_rank + 15) / 16);
-    const uint32_t grid = grid_of(jobs, (uint64_t)device_cus * 16);
-    hipLaunchKernelGGL(shrink_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
+    const uint32_t grid = (uint32_t)(lora_slots(a.m, a.n_adapters) * parts);
+    hipLaunchKernelGGL(shrink_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a, parts);
     return launched(EIDM_KERNEL_LORA_SHRINK, grid, 256, 0);
 }
 
 template <int DT, int RG>
 hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
     const uint32_t parts = (a.max_rank + 15) / 16, shrinks = with_shrink ? a.m * parts : 0;
-    const uint32_t blocks = (a.n + 15) / 16;
-    uint32_t lds = RG >= 0 ? a.m * few_row_floats(a.k) * 4 : rows16_lds(-RG) * 4;
+    constexpr uint32_t T = RG < 0 ? -RG : 1;
+    const uint32_t ctiles = (a.n + 16 * T - 1) / (16 * T), rtiles = (a.m + 16 * T - 1) / (16 * T);
+    const uint32_t blocks = RG >= 0 ? ctiles : (ctiles + 7) / 8 * 8 * rtiles;
+    uint32_t lds = RG >= 0 ? a.m * few_row_floats(a.k) * 4 : rows16_lds(T * T) * 4;
     if (with_shrink && lds < few_row_floats(a.k) * 4) lds = few_row_floats(a.k) * 4;
     hipLaunchKernelGGL((base_few_kernel<DT, RG>), dim3(shrinks + blocks), dim3(256), lds, stream, a, weights, shrinks,
                        parts);
@@ -303,29 +321,36 @@ hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink,
 }
 
 template <int DT>
-hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
+hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, int device_cus, hipStream_t stream) {
     if (a.m <= 4 && stages_rows(a.m, a.k))
         return a.m == 1 ? base_few<DT, 0>(a, weights, with_shrink, stream)
                         : base_few<DT, 1>(a, weights, with_shrink, stream);
-    if (a.m <= 16) return base_few<DT, -1>(a, weights, with_shrink, stream);
-    if (a.m <= 32) return base_few<DT, -2>(a, weights, with_shrink, stream);
-    return base_few<DT, -4>(a, weights, with_shrink, stream);
+    // 16x16 tiles until they fill the device twice: more blocks; then 32x32:
+    // half the activation and weight traffic per product
+    const uint64_t tiles = ((uint64_t)a.m + 15) / 16 * ((a.n + 15) / 16);
+    if (tiles < (uint64_t)device_cus * 2) return base_few<DT, -1>(a, weights, with_shrink, stream);
+    return base_few<DT, -2>(a, weights, with_shrink, stream);
 }
 
 template <int DT>
 hipError_t expand_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
-    if (a.m <= kRowForm) {
+    if (!a.rows) {
         const uint32_t grid = grid_of((uint64_t)a.m * ((a.n + 255) / 256), (uint64_t)device_cus * 32);
         hipLaunchKernelGGL(expand_row_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
         return launched(EIDM_KERNEL_LORA_EXPAND, grid, 256, 0);
     }
-    const uint64_t jobs = ((uint64_t)a.m + 15) / 16 * ((a.n + 63) / 64);
-    const uint32_t grid = grid_of((jobs + 3) / 4, (uint64_t)device_cus * 64);
-    hipLaunchKernelGGL(expand_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a);
+    const uint32_t parts = (a.n + 255) / 256, grid = (uint32_t)(lora_slots(a.m, a.n_adapters) * parts);
+    hipLaunchKernelGGL(expand_tile_kernel<DT>, dim3(grid), dim3(256), 0, stream, a, parts);
     return launched(EIDM_KERNEL_LORA_EXPAND, grid, 256, 0);
 }
 
 }  // namespace
+
+bool lora_sorts_rows(uint32_t m, uint32_t k, uint32_t max_rank) {
+    // measured on k = 768 .. 4096: rank 16 crosses between 500 and 1000 rows,
+    // rank 64 at 200
+    return (m > kLoraRowForm && (uint64_t)m * max_rank > 12288) || !stages_rows(1, k);
+}
 
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream) {
     switch (a.dtype) {
@@ -336,19 +361,23 @@ hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t str
     }
 }
 
-bool lora_base_few_supported(const LoraArgs& a) { return a.m <= kRowForm; }
+// The library's Grouped kernels take over where the 32x32 tiles fill the
+// device more than three times (they share activations through LDS).
+bool lora_base_few_supported(const LoraArgs& a, int device_cus) {
+    return ((uint64_t)a.m + 31) / 32 * ((a.n + 31) / 32) <= (uint64_t)device_cus * 3;
+}
 
 hipError_t launch_lora_base_few(const LoraArgs& a, int weight_dtype, const uint8_t* weights, int device_cus,
                                 hipStream_t stream) {
-    const bool together = weight_dtype == a.dtype && stages_rows(1, a.k);
+    const bool together = weight_dtype == a.dtype && !a.rows;
     if (!together) {
         const hipError_t err = launch_lora_shrink(a, device_cus, stream);
         if (err != hipSuccess) return err;
     }
     switch (weight_dtype) {
-    case kDtypeF32: return base_few_dt<kDtypeF32>(a, weights, together, stream);
-    case kDtypeF16: return base_few_dt<kDtypeF16>(a, weights, together, stream);
-    case kDtypeBF16: return base_few_dt<kDtypeBF16>(a, weights, together, stream);
+    case kDtypeF32: return base_few_dt<kDtypeF32>(a, weights, together, device_cus, stream);
+    case kDtypeF16: return base_few_dt<kDtypeF16>(a, weights, together, device_cus, stream);
+    case kDtypeBF16: return base_few_dt<kDtypeBF16>(a, weights, together, device_cus, stream);
     default: return hipErrorInvalidValue;
     }
 }
@@ -371,7 +400,9 @@ uint32_t size_of(int dtype) { return dtype == EIDM_DTYPE_F32 ? 4 : 2; }
 
 struct LoraSizes {
     uint64_t weights, a, b;                   // extents needed, bytes
-    uint64_t off_ids, off_matmul, matmul, total;  // scratch: v | ids of the shared projection | its own scratch
+    // scratch: v | sort (histograms, counts, offsets, rows, tiles) | ids of the shared
+    // projection | its own scratch
+    uint64_t off_hist, off_counts, off_offsets, off_rows, off_tiles, off_ids, off_matmul, matmul, total;
     uint32_t v_stride;
 };
 
@@ -423,7 +454,18 @@ int lora_sizes(const eidm_lora_shape* f, bool shared, LoraSizes* z) {
     if (f->max_rank > kMaxLoraRank)
         return api_fail(EIDM_E_UNSUPPORTED, "max_rank %u above the supported %u", f->max_rank, kMaxLoraRank);
     z->v_stride = (f->max_rank + 7) / 8 * 8;
-    z->off_ids = align256((uint64_t)f->m * z->v_stride * 4);
+    z->off_hist = align256((uint64_t)f->m * z->v_stride * 4);
+    z->off_counts = z->off_offsets = z->off_rows = z->off_tiles = z->off_ids = z->off_hist;
+    if (lora_sorts_rows(f->m, f->k, f->max_rank)) {
+        const uint64_t parts = ((uint64_t)f->n + 255) / 256;  // a launch has a block per slot and part
+        if (lora_slots(f->m, f->n_adapters) * parts > 0x7fffffffull)
+            return api_fail(EIDM_E_UNSUPPORTED, "the adapters' grid for %u rows of %u columns is too large", f->m, f->n);
+        z->off_counts = z->off_hist + align256(map_hist_elements(f->m, f->n_adapters) * 4);
+        z->off_offsets = z->off_counts + align256((uint64_t)(f->n_adapters + 1) * 4);
+        z->off_rows = z->off_offsets + align256((uint64_t)(f->n_adapters + 2) * 4);
+        z->off_tiles = z->off_rows + align256((uint64_t)f->m * 4);
+        z->off_ids = z->off_tiles + align256(lora_slots(f->m, f->n_adapters) * kTileWords * 4);
+    }
     z->off_matmul = z->off_ids + align256((uint64_t)f->m * 4);
     z->weights = z->matmul = 0;
     if (shared) {
@@ -510,14 +552,24 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
     a.base = weights ? output : base;
     a.v = reinterpret_cast<float*>(ws);
     a.out = output;
+    const int cus = eidm::device_cus();
     hipError_t err;
-    if (weights && shape->arith == EIDM_ARITH_F32 && eidm::lora_base_few_supported(a)) {
-        err = eidm::launch_lora_base_few(a, shape->weight_dtype, static_cast<const uint8_t*>(weights),
-                                         eidm::device_cus(), st);
+    if (eidm::lora_sorts_rows(a.m, a.k, a.max_rank)) {
+        auto at = [&](uint64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
+        const eidm::MapBuffers buf{at(z.off_hist), at(z.off_counts), at(z.off_offsets), at(z.off_rows)};
+        err = eidm::launch_map(adapter_ids, a.m, a.n_adapters, buf, st);
+        if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "map launch: %s", hipGetErrorString(err));
+        a.counts = buf.counts;
+        a.offsets = buf.offsets;
+        a.rows = buf.rows;
+        a.tiles = at(z.off_tiles);
+    }
+    if (weights && shape->arith == EIDM_ARITH_F32 && eidm::lora_base_few_supported(a, cus)) {
+        err = eidm::launch_lora_base_few(a, shape->weight_dtype, static_cast<const uint8_t*>(weights), cus, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "projection launch: %s", hipGetErrorString(err));
     } else {
         if (weights) a.zero_ids = reinterpret_cast<uint32_t*>(ws + z.off_ids);
-        err = eidm::launch_lora_shrink(a, eidm::device_cus(), st);
+        err = eidm::launch_lora_shrink(a, cus, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter shrink launch: %s", hipGetErrorString(err));
         if (weights) {
             const eidm_shape s = eidm::shared_projection(shape);
@@ -526,7 +578,7 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
             if (rc) return rc;
         }
     }
-    err = eidm::launch_lora_expand(a, eidm::device_cus(), st);
+    err = eidm::launch_lora_expand(a, cus, st);
     if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter expand launch: %s", hipGetErrorString(err));
     return eidm::api_ok();
 }

@@ -182,14 +182,14 @@ __device__ __forceinline__ void expert_major(const FewMap& map, float* xs, bool 
                 weight_of(uniform(map.id[u]), uniform(job) - u * groups, to);
             };
             uint32_t job = pos + (threadIdx.x >> 6);
-            if (job < stop) {
-                weights_at(job, wrow);
-                w.start(wrow, (int)k);
-            }
+            auto stage = few_stage<8>(xs, staged ? 0 : limit - base, k,
+                                      [&](uint32_t i) { return row_of(map.row[base + i]); });
+            stage.issue();  // ahead of the weights: a thread's loads return in order
+            // in every wavefront: behind a branch, the rows' wait would be for the weights too
+            weights_at(min(job, stop - 1), wrow);
+            w.start(wrow, (int)k);
             if (!staged) {
                 __syncthreads();  // the rows of the pass before are done with
-                auto stage = few_stage<8>(xs, limit - base, k, [&](uint32_t i) { return row_of(map.row[base + i]); });
-                stage.issue();
                 stage.finish();
                 __syncthreads();
             }
@@ -331,10 +331,8 @@ __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs
     FewStream<DT, 2, few_depth<DT, 2>(LOADS), true> w;
     const uint8_t* wrow[2];
     uint32_t u = uniform(threadIdx.x >> 6);
-    if (u < used) {
-        weights_at(u, wrow);
-        w.start(wrow, (int)a.inter);
-    }
+    weights_at(min(u, used - 1), wrow);
+    w.start(wrow, (int)a.inter);
     stage.finish();
     __syncthreads();
     for (; u < used; u += kWaves) {

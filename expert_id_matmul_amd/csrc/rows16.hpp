@@ -1,4 +1,4 @@
-// rows16.hpp -- a block of four wavefronts: 16*RT activation rows times 16
+// rows16.hpp -- a block of four wavefronts: 16*RT activation rows times 16*CT
 // weight rows (output columns), both streamed from memory, in the library's
 // fixed reduction order; used by the adapters' and the shared projection's
 // products of a few rows.
@@ -26,38 +26,42 @@ constexpr int kTileRows = 16;
 constexpr int kTileWaves = 4;
 
 // LDS floats of rows16_product
-constexpr uint32_t rows16_lds(int row_tiles) { return (uint32_t)row_tiles * kTileWaves * 16 * 64; }
+constexpr uint32_t rows16_lds(int tiles) { return (uint32_t)tiles * kTileWaves * 16 * 64; }
 
-// wrow: this lane's weight row (row l%16), xrow[t]: its activation row of row
-// tile t; lanes without one repeat a valid row.  On return total[t] of lane l
-// of wavefront v is (row 4*(l/16)+v of tile t, column l%16).  The block's
-// four wavefronts call it together; xs (rows16_lds(RT) floats) may be reused
-// after the next barrier.
-template <int DT, int RT, int D, bool NT>
-__device__ __forceinline__ void rows16_product(const uint8_t* wrow, const float* const (&xrow)[RT], int k, float* xs,
-                                               float (&total)[RT]) {
+// wrow[c]: this lane's weight row (row l%16 of column tile c), xrow[t]: its
+// activation row of row tile t; lanes without one repeat a valid row.  On
+// return total[t][c] of lane l of wavefront v is (row 4*(l/16)+v of tile t,
+// column l%16 of tile c).  The block's four wavefronts call it together; xs
+// (rows16_lds(RT*CT) floats) may be reused after the next barrier.
+template <int DT, int RT, int CT, int D, bool NT>
+__device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT], const float* const (&xrow)[RT], int k,
+                                               float* xs, float (&total)[RT][CT]) {
     constexpr int S = DtypeSize<DT>::value;
     constexpr int NP = S / 2;
     const int lane = threadIdx.x & 63, s = lane >> 4;
     const int j = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int full = k / kRoundK;
 
-    f32x16 acc[RT];
+    f32x16 acc[RT][CT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x16{};
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[t][c] = f32x16{};
 
     struct Slot {
-        fr_u32x4 w[NP];
+        fr_u32x4 w[CT][NP];
         f32x4 x[RT][2];
     };
     const int at0 = j * 32 + s * kGranule;  // this lane's elements of a round
     auto fetch = [&](int r, Slot& t) {
         const size_t at = (size_t)r * kRoundK + at0;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow + at * S + 16 * i);
-            t.w[i] = NT ? __builtin_nontemporal_load(p) : *p;
-        }
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at * S + 16 * i);
+                t.w[c][i] = NT ? __builtin_nontemporal_load(p) : *p;
+            }
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
             t.x[u][0] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[u] + at);
@@ -65,13 +69,16 @@ __device__ __forceinline__ void rows16_product(const uint8_t* wrow, const float*
         }
     };
     auto consume = [&](const Slot& t) {
-        float w[kGranule];
-        few_widen<DT>(t.w, w);
+        float w[CT][kGranule];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) few_widen<DT>(t.w[c], w[c]);
 #pragma unroll
         for (int i = 0; i < kGranule; ++i)
 #pragma unroll
             for (int u = 0; u < RT; ++u)
-                acc[u] = __builtin_amdgcn_mfma_f32_16x16x1f32(t.x[u][i / 4][i % 4], w[i], acc[u], 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    acc[u][c] = __builtin_amdgcn_mfma_f32_16x16x1f32(t.x[u][i / 4][i % 4], w[c][i], acc[u][c], 0, 0, 0);
     };
 
     Slot ring[D];
@@ -93,11 +100,14 @@ __device__ __forceinline__ void rows16_product(const uint8_t* wrow, const float*
                 if (kk + i < k) {
 #pragma unroll
                     for (int u = 0; u < RT; ++u) tail.x[u][i / 4][i % 4] = xrow[u][kk + i];
-                    if constexpr (S == 4)
-                        tail.w[i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(wrow + (size_t)(kk + i) * 4);
-                    else
-                        tail.w[0][i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(wrow + (size_t)(kk + i) * 2)
-                                            << (i % 2 * 16);
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        if constexpr (S == 4)
+                            tail.w[c][i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(wrow[c] + (size_t)(kk + i) * 4);
+                        else
+                            tail.w[c][0][i / 2] |=
+                                (uint32_t)*reinterpret_cast<const uint16_t*>(wrow[c] + (size_t)(kk + i) * 2) << (i % 2 * 16);
+                    }
                 }
         }
     }
@@ -122,22 +132,25 @@ __device__ __forceinline__ void rows16_product(const uint8_t* wrow, const float*
 
     // pairs (slice, slice^8), then ^4: the wavefronts; ^2, ^1: the blocks
     __syncthreads();  // xs is free
-    f32x4* mine = reinterpret_cast<f32x4*>(xs) + (size_t)j * RT * 4 * 64 + lane;
+    constexpr int T = RT * CT;
+    f32x4* mine = reinterpret_cast<f32x4*>(xs) + (size_t)j * T * 4 * 64 + lane;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int v = 0; v < 4; ++v)  // the four blocks' sums of one output together
-            mine[(t * 4 + v) * 64] = f32x4{acc[t][v], acc[t][4 + v], acc[t][8 + v], acc[t][12 + v]};
+        for (int v = 0; v < 4; ++v) {  // the four blocks' sums of one output together
+            const f32x16& e = acc[t / CT][t % CT];
+            mine[(t * 4 + v) * 64] = f32x4{e[v], e[4 + v], e[8 + v], e[12 + v]};
+        }
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
+    for (int t = 0; t < T; ++t) {
         const f32x4* p = reinterpret_cast<const f32x4*>(xs) + (t * 4 + j) * 64 + lane;
-        constexpr int W = RT * 4 * 64;
+        constexpr int W = T * 4 * 64;
         const f32x4 a = p[0], b = p[W], c = p[2 * W], d = p[3 * W];
         f32x4 q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) q[i] = (a[i] + c[i]) + (b[i] + d[i]);
-        total[t] = (q[0] + q[2]) + (q[1] + q[3]);
+        total[t / CT][t % CT] = (q[0] + q[2]) + (q[1] + q[3]);
     }
 }
 
