@@ -69,9 +69,10 @@ __global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t pa
 }
 
 // The shared projection (a.out = W x) and, in the last `shrinks` blocks of
-// the same launch, the row form's shrink, which needs none of it.  RG 0, 1 (one row, up to four): rows staged in LDS, each
-// wavefront four columns; else blocks of 16*T rows by 16*T columns, T = -RG.
-template <int DT, int RG>
+// the same launch, the row form's shrink, which needs none of it.  CT = 0:
+// RT row groups staged in LDS (0: one row, 1: up to four), each wavefront four
+// columns; else blocks of 16*RT rows by 16*CT columns.
+template <int DT, int RT, int CT>
 __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t* weights, uint32_t shrinks,
                                                        uint32_t parts) {
     extern __shared__ __align__(16) float xs[];
@@ -80,9 +81,8 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
         shrink_row<DT>(a, (block - bases) / parts, (block - bases) % parts, xs);
         return;
     }
-    if constexpr (RG >= 0) {
+    if constexpr (CT == 0) {
         const uint32_t q = lane & 3, col = block * 16 + (threadIdx.x >> 6) * 4 + q;
-        const bool live = col - q < a.n;  // wave-uniform
         const uint8_t* const wrow[1] = {weights + (size_t)min(col, a.n - 1) * a.k * DtypeSize<DT>::value};
         FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 4 : 8, true> w;
         auto stage = few_stage<8>(xs, a.m, a.k, [&](uint32_t t) { return a.x + (size_t)t * a.k; });
@@ -90,33 +90,32 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
         w.start(wrow, (int)a.k);
         stage.finish();
         __syncthreads();
-        if (!live) return;
-        few_rows_tile<RG, false>(w, wrow, wrow, xs, few_row_floats(a.k), a.m, (int)a.k, [](uint32_t i) { return i; },
+        if (col - q >= a.n) return;  // wave-uniform
+        few_rows_tile<RT, false>(w, wrow, wrow, xs, few_row_floats(a.k), a.m, (int)a.k, [](uint32_t i) { return i; },
                                  [&](uint32_t t, const float (&v)[1]) {
                                      if (col < a.n) a.out[(size_t)t * a.n + col] = v[0];
                                  });
     } else {
         // block (column tile, row tile), the row tiles of one column tile on
         // one XCD, whose L2 then serves the weights to all but the first
-        constexpr int T = -RG;
-        const uint32_t rtiles = (a.m + 16 * T - 1) / (16 * T), i = lane & 15;
+        const uint32_t rtiles = (a.m + 16 * RT - 1) / (16 * RT), i = lane & 15;
         const uint32_t group = block / (8 * rtiles), in = block % (8 * rtiles);
-        const uint32_t col0 = (group * 8 + in % 8) * 16 * T, row0 = in / 8 * 16 * T;
+        const uint32_t col0 = (group * 8 + in % 8) * 16 * CT, row0 = in / 8 * 16 * RT;
         if (col0 >= a.n) return;  // the last group of column tiles
-        const uint8_t* wrow[T];
-        const float* xrow[T];
+        const uint8_t* wrow[CT];
+        const float* xrow[RT];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            wrow[t] = weights + (size_t)min(col0 + t * 16 + i, a.n - 1) * a.k * DtypeSize<DT>::value;
-            xrow[t] = a.x + (size_t)min(row0 + t * 16 + i, a.m - 1) * a.k;
-        }
-        float total[T][T];
-        rows16_product<DT, T, T, T == 1 ? 8 : 4, false>(wrow, xrow, (int)a.k, xs, total);
+        for (int c = 0; c < CT; ++c)
+            wrow[c] = weights + (size_t)min(col0 + c * 16 + i, a.n - 1) * a.k * DtypeSize<DT>::value;
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+        for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(row0 + t * 16 + i, a.m - 1) * a.k;
+        float total[RT][CT];
+        rows16_product<DT, RT, CT, RT * CT == 1 ? 8 : RT * CT == 2 ? 6 : 4, false>(wrow, xrow, (int)a.k, xs, total);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
             const uint32_t r = row0 + t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
 #pragma unroll
-            for (int c = 0; c < T; ++c)
+            for (int c = 0; c < CT; ++c)
                 if (r < a.m && col0 + c * 16 + i < a.n) a.out[(size_t)r * a.n + col0 + c * 16 + i] = total[t][c];
         }
     }
@@ -307,29 +306,39 @@ hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
     return launched(EIDM_KERNEL_LORA_SHRINK, grid, 256, 0);
 }
 
-template <int DT, int RG>
+template <int DT, int RT, int CT>
 hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
     const uint32_t parts = (a.max_rank + 15) / 16, shrinks = with_shrink ? a.m * parts : 0;
-    constexpr uint32_t T = RG < 0 ? -RG : 1;
-    const uint32_t ctiles = (a.n + 16 * T - 1) / (16 * T), rtiles = (a.m + 16 * T - 1) / (16 * T);
-    const uint32_t blocks = RG >= 0 ? ctiles : (ctiles + 7) / 8 * 8 * rtiles;
-    uint32_t lds = RG >= 0 ? a.m * few_row_floats(a.k) * 4 : rows16_lds(T * T) * 4;
+    constexpr uint32_t C = CT ? 16 * CT : 16, R = CT ? 16 * RT : 1;
+    const uint32_t ctiles = (a.n + C - 1) / C, rtiles = (a.m + R - 1) / R;
+    const uint32_t blocks = CT ? (ctiles + 7) / 8 * 8 * rtiles : ctiles;
+    uint32_t lds = CT ? rows16_lds(RT * CT) * 4 : a.m * few_row_floats(a.k) * 4;
     if (with_shrink && lds < few_row_floats(a.k) * 4) lds = few_row_floats(a.k) * 4;
-    hipLaunchKernelGGL((base_few_kernel<DT, RG>), dim3(shrinks + blocks), dim3(256), lds, stream, a, weights, shrinks,
-                       parts);
+    hipLaunchKernelGGL((base_few_kernel<DT, RT, CT>), dim3(shrinks + blocks), dim3(256), lds, stream, a, weights,
+                       shrinks, parts);
     return launched(EIDM_KERNEL_LORA_BASE, shrinks + blocks, 256, lds);
+}
+
+// Relative time of the busiest compute unit when the tiles of 16*rt x 16*ct
+// are spread evenly, `each` the time of one.
+uint64_t makespan(const LoraArgs& a, uint32_t rt, uint32_t ct, uint32_t each, uint32_t cus) {
+    const uint64_t tiles = ((uint64_t)a.m + 16 * rt - 1) / (16 * rt) * ((a.n + 16 * ct - 1) / (16 * ct));
+    return (tiles + cus - 1) / cus * each;
 }
 
 template <int DT>
 hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, int device_cus, hipStream_t stream) {
     if (a.m <= 4 && stages_rows(a.m, a.k))
-        return a.m == 1 ? base_few<DT, 0>(a, weights, with_shrink, stream)
-                        : base_few<DT, 1>(a, weights, with_shrink, stream);
-    // 16x16 tiles until they fill the device twice: more blocks; then 32x32:
-    // half the activation and weight traffic per product
-    const uint64_t tiles = ((uint64_t)a.m + 15) / 16 * ((a.n + 15) / 16);
-    if (tiles < (uint64_t)device_cus * 2) return base_few<DT, -1>(a, weights, with_shrink, stream);
-    return base_few<DT, -2>(a, weights, with_shrink, stream);
+        return a.m == 1 ? base_few<DT, 0, 0>(a, weights, with_shrink, stream)
+                        : base_few<DT, 1, 0>(a, weights, with_shrink, stream);
+    // larger tiles read less per product, smaller ones spread more evenly; one
+    // tile of each kind per compute unit takes 12, 17 and 23.5 us at k = 4096
+    // (6, 9 and 13 at k = 2048)
+    const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
+    const uint64_t one = makespan(a, 1, 1, 24, cus), two = makespan(a, 1, 2, 34, cus), four = makespan(a, 2, 2, 48, cus);
+    if (one <= two && one <= four) return base_few<DT, 1, 1>(a, weights, with_shrink, stream);
+    return two <= four ? base_few<DT, 1, 2>(a, weights, with_shrink, stream)
+                       : base_few<DT, 2, 2>(a, weights, with_shrink, stream);
 }
 
 template <int DT>

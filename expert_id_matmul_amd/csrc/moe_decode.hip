@@ -17,6 +17,7 @@
 // cortiq-engine 0.7.7, src/mimo_moe.rs, Dynamic::run (route, one FFN per
 // pick, weighted sum); hf2q dense_ffn_arena.rs, MoeFfnArena (gate, up, h, y).
 #include <atomic>
+#include <cmath>
 
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
@@ -48,23 +49,24 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
-// ------------------------------------------------------------ one token
-// A wavefront per slot; a block owns `cols` <= 4 columns of h for every slot
-// (so all compute units have the same share of each expert).  Routing as in
-// the fused decode step (moe_direct.hip): each expert's sigmoid by one
-// thread, every wavefront runs the selection up to its own pick, the last
-// one forms the gates.
+// ------------------------------------------------------- one token by itself
+// A wavefront per slot; a block owns `cols` <= 4 columns of one token's h for
+// every slot (so all compute units have the same share of each expert).
+// Routing as in the fused decode step (moe_direct.hip): each expert's sigmoid
+// by one thread, every wavefront runs the selection up to its own pick, the
+// last one forms the gates.
 template <int DT, int NV, int MAXW>
-__global__ __launch_bounds__(64 * MAXW) void gate_up_one_kernel(MoeDecodeArgs a, uint32_t cols) {
+__global__ __launch_bounds__(64 * MAXW) void gate_up_one_kernel(MoeDecodeArgs a, uint32_t cols, uint32_t blocks) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) float xs[];
     __shared__ float rs_s[64 * NV];
     __shared__ uint32_t rs_code[64 * NV];
     const uint32_t lane = threadIdx.x & 63, slot = threadIdx.x >> 6, q = lane & 3;
+    const uint32_t token = blockIdx.x / blocks, block = blockIdx.x % blocks;
     RouteInputs<NV> rin;
-    route_inputs_issue<NV>(a.logits, a.bias, a.n_experts, rin);
+    route_inputs_issue<NV>(a.logits + (size_t)token * a.n_experts, a.bias, a.n_experts, rin);
     __builtin_amdgcn_sched_barrier(0);  // the row's loads queue behind the router's
-    auto stage = few_stage<8>(xs, 1, a.hidden, [&](uint32_t) { return a.x; });
+    auto stage = few_stage<8>(xs, 1, a.hidden, [&](uint32_t) { return a.x + (size_t)token * a.hidden; });
     stage.issue();
     __builtin_amdgcn_sched_barrier(0);
     route_inputs_score<NV>(rin, a.n_experts, rs_s, rs_code);
@@ -76,54 +78,55 @@ __global__ __launch_bounds__(64 * MAXW) void gate_up_one_kernel(MoeDecodeArgs a,
     uint32_t pick;
     float score;
     const float sum = route_select<NV>(sc, slot + 1, pick, score);
-    if (blockIdx.x == 0 && slot == a.top_k - 1 && lane < a.top_k) {
-        a.ids[lane] = pick;
-        a.gates[lane] = a.renormalize ? __fdiv_rn(score, sum) : score;
+    if (block == 0 && slot == a.top_k - 1 && lane < a.top_k) {
+        a.ids[token * a.top_k + lane] = pick;
+        a.gates[token * a.top_k + lane] = a.renormalize ? __fdiv_rn(score, sum) : score;
     }
     const uint32_t e = (uint32_t)__builtin_amdgcn_readlane((int)pick, (int)slot);
-    const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.inter);
+    const uint32_t col0 = block * cols, end = min(col0 + cols, a.inter);
     const uint32_t col = col0 + q;
     const size_t at = (size_t)e * a.gate_up_stride + (size_t)(col < end ? col : col0) * a.hidden * S;
     const uint8_t* const wrow[2] = {a.w_gate + at, a.w_up + at};
     FewStream<DT, 2, few_depth<DT, 2>(MAXW > 8 ? 12 : 16), true> w;
     w.start(wrow, (int)a.hidden);
     few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.hidden, [](uint32_t) { return 0u; },
-                     [&](uint32_t, const float (&t)[2]) {
-                         if (col < end) a.h[(size_t)slot * a.inter + col] = silu_mul(t[0], t[1]);
-                     });
+                            [&](uint32_t, const float (&t)[2]) {
+                                if (col < end) a.h[(size_t)(token * a.top_k + slot) * a.inter + col] = silu_mul(t[0], t[1]);
+                            });
 }
 
-// A wavefront per slot; a block owns `cols` <= 8 output columns.
-template <int DT, int LOADS, int MAXW>
-__global__ __launch_bounds__(64 * MAXW) void down_one_kernel(MoeDecodeArgs a, uint32_t cols) {
+// A wavefront per slot; a block owns `cols` <= 4*C output columns of a token.
+template <int DT, int C, int LOADS, int MAXW>
+__global__ __launch_bounds__(64 * MAXW) void down_one_kernel(MoeDecodeArgs a, uint32_t cols, uint32_t blocks) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) float xs[];
-    __shared__ float ys[MAXW][8];
+    __shared__ float ys[MAXW][4 * C];
     const uint32_t lane = threadIdx.x & 63, slot = threadIdx.x >> 6, q = lane & 3;
-    const uint32_t e = uniform(a.ids[slot]);
-    auto stage = few_stage<8>(xs, a.top_k, a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; });
+    const uint32_t token = blockIdx.x / blocks, first = token * a.top_k;  // its first routed row
+    const uint32_t e = uniform(a.ids[first + slot]);
+    auto stage = few_stage<8>(xs, a.top_k, a.inter, [&](uint32_t r) { return a.h + (size_t)(first + r) * a.inter; });
     stage.issue();
-    const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.hidden);
-    const uint8_t* wrow[2];
+    const uint32_t col0 = blockIdx.x % blocks * cols, end = min(col0 + cols, a.hidden);
+    const uint8_t* wrow[C];
 #pragma unroll
-    for (uint32_t c = 0; c < 2; ++c) {
+    for (uint32_t c = 0; c < C; ++c) {
         const uint32_t col = col0 + 4 * c + q;
         wrow[c] = a.w_down + (size_t)e * a.down_stride + (size_t)(col < end ? col : col0) * a.inter * S;
     }
-    FewStream<DT, 2, few_depth<DT, 2>(LOADS), true> w;
+    FewStream<DT, C, few_depth<DT, C>(LOADS), true> w;
     w.start(wrow, (int)a.inter);
     stage.finish();
     __syncthreads();
     few_rows_tile<0, false>(w, wrow, wrow, xs, few_row_floats(a.inter), 1, (int)a.inter, [&](uint32_t) { return slot; },
-                     [&](uint32_t, const float (&t)[2]) {
-                         ys[slot][q] = t[0];
-                         ys[slot][4 + q] = t[1];
-                     });
+                            [&](uint32_t, const float (&t)[C]) {
+#pragma unroll
+                                for (int c = 0; c < C; ++c) ys[slot][4 * c + q] = t[c];
+                            });
     __syncthreads();
     if (slot == 0 && col0 + lane < end) {
         float acc = 0.0f;
-        for (uint32_t s = 0; s < a.top_k; ++s) acc = __builtin_fmaf(a.gates[s], ys[s][lane], acc);
-        a.out[col0 + lane] = acc;
+        for (uint32_t s = 0; s < a.top_k; ++s) acc = __builtin_fmaf(a.gates[first + s], ys[s][lane], acc);
+        a.out[(size_t)token * a.hidden + col0 + lane] = acc;
     }
 }
 
@@ -304,16 +307,16 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(MoeDecodeArgs a) {
         });
 }
 
-// Few rows: all of h staged; a block owns `cols` <= 8 output columns of
+// Few rows: all of h staged; a block owns `cols` <= 4*C output columns of
 // every token, its wavefronts take the touched experts in turn.
-template <int DT, int LOADS>
+template <int DT, int C, int LOADS>
 __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs a, uint32_t cols) {
     constexpr int S = DtypeSize<DT>::value;
     extern __shared__ __align__(16) uint32_t lds[];
     const uint32_t rows = a.m * a.top_k;
     const FewMap map = few_map_at(lds, rows, a.n_experts);
-    float* ys = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));  // [rows][8]
-    float* xs = ys + rows * 8;
+    float* ys = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));  // [rows][4*C]
+    float* xs = ys + rows * 4 * C;
     auto stage = few_stage<8>(xs, rows, a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; });
     stage.issue();
     few_map_build(map, a.ids, rows, a.n_experts, [](uint32_t) { return 1u; });
@@ -321,15 +324,15 @@ __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs
     const uint32_t q = threadIdx.x & 3;
     const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.hidden);
     const uint32_t used = *map.used;
-    auto weights_at = [&](uint32_t u, const uint8_t* (&to)[2]) {
+    auto weights_at = [&](uint32_t u, const uint8_t* (&to)[C]) {
 #pragma unroll
-        for (uint32_t c = 0; c < 2; ++c) {
+        for (uint32_t c = 0; c < C; ++c) {
             const uint32_t col = col0 + 4 * c + q;
             to[c] = a.w_down + (size_t)uniform(map.id[u]) * a.down_stride + (size_t)(col < end ? col : col0) * a.inter * S;
         }
     };
-    FewStream<DT, 2, few_depth<DT, 2>(LOADS), true> w;
-    const uint8_t* wrow[2];
+    FewStream<DT, C, few_depth<DT, C>(LOADS), true> w;
+    const uint8_t* wrow[C];
     uint32_t u = uniform(threadIdx.x >> 6);
     weights_at(min(u, used - 1), wrow);
     w.start(wrow, (int)a.inter);
@@ -341,29 +344,31 @@ __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs
             const bool again = at + kFewRows < to;
             const uint32_t count = min(to - at, (uint32_t)kFewRows), stride = few_row_floats(a.inter);
             auto lds_row = [&](uint32_t i) { return map.row[at + i]; };
-            auto emit = [&](uint32_t i, const float (&t)[2]) {
-                ys[map.row[at + i] * 8 + q] = t[0];
-                ys[map.row[at + i] * 8 + 4 + q] = t[1];
+            auto emit = [&](uint32_t i, const float (&t)[C]) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) ys[map.row[at + i] * (4 * C) + 4 * c + q] = t[c];
             };
-            const uint8_t* next[2] = {wrow[0], wrow[1]};
+            const uint8_t* next[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) next[c] = wrow[c];
             if (again || u + kWaves < used) {
                 if (!again) weights_at(u + kWaves, next);
                 few_rows_any<true>(w, wrow, next, xs, stride, count, (int)a.inter, lds_row, emit);
-                wrow[0] = next[0];
-                wrow[1] = next[1];
+#pragma unroll
+                for (int c = 0; c < C; ++c) wrow[c] = next[c];
             } else {
                 few_rows_any<false>(w, wrow, next, xs, stride, count, (int)a.inter, lds_row, emit);
             }
         }
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < a.m * 8; i += blockDim.x) {
-        const uint32_t t = i / 8, c = i % 8;
+    for (uint32_t i = threadIdx.x; i < a.m * 4 * C; i += blockDim.x) {
+        const uint32_t t = i / (4 * C), c = i % (4 * C);
         if (col0 + c < end) {
             float acc = 0.0f;
             for (uint32_t s = 0; s < a.top_k; ++s) {
                 const uint32_t r = t * a.top_k + s;
-                acc = __builtin_fmaf(a.gates[r], ys[r * 8 + c], acc);
+                acc = __builtin_fmaf(a.gates[r], ys[r * (4 * C) + c], acc);
             }
             a.out[(size_t)t * a.hidden + col0 + c] = acc;
         }
@@ -418,32 +423,49 @@ bool twelve_loads(int dtype, uint32_t k, uint32_t weight_rows) {
 }
 
 template <int DT>
-hipError_t launch_one_token(const MoeDecodeArgs& a, uint32_t cus, hipStream_t stream) {
+hipError_t launch_each_token(const MoeDecodeArgs& a, uint32_t cus, hipStream_t stream) {
     const uint32_t threads = 64 * a.top_k;
     const uint32_t up = block_columns(a.inter, 4, cus), down = block_columns(a.hidden, 8, cus);
-    const uint32_t up_blocks = (a.inter + up - 1) / up, down_blocks = (a.hidden + down - 1) / down;
+    const uint32_t ub = (a.inter + up - 1) / up, db = (a.hidden + down - 1) / down;  // blocks per token
     const uint32_t up_lds = few_row_floats(a.hidden) * 4, down_lds = a.top_k * few_row_floats(a.inter) * 4;
     constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN;
     const bool wide = a.top_k > 8;
     hipError_t err;
     if (a.n_experts <= 256)
-        err = wide ? launch_one<gate_up_one_kernel<DT, 4, 16>>(U, up_blocks, threads, up_lds, stream, a, up)
-                   : launch_one<gate_up_one_kernel<DT, 4, 8>>(U, up_blocks, threads, up_lds, stream, a, up);
+        err = wide ? launch_one<gate_up_one_kernel<DT, 4, 16>>(U, ub * a.m, threads, up_lds, stream, a, up, ub)
+                   : launch_one<gate_up_one_kernel<DT, 4, 8>>(U, ub * a.m, threads, up_lds, stream, a, up, ub);
     else
-        err = wide ? launch_one<gate_up_one_kernel<DT, 32, 16>>(U, up_blocks, threads, up_lds, stream, a, up)
-                   : launch_one<gate_up_one_kernel<DT, 32, 8>>(U, up_blocks, threads, up_lds, stream, a, up);
+        err = wide ? launch_one<gate_up_one_kernel<DT, 32, 16>>(U, ub * a.m, threads, up_lds, stream, a, up, ub)
+                   : launch_one<gate_up_one_kernel<DT, 32, 8>>(U, ub * a.m, threads, up_lds, stream, a, up, ub);
     if (err != hipSuccess) return err;
-    if (wide) return launch_one<down_one_kernel<DT, 12, 16>>(W, down_blocks, threads, down_lds, stream, a, down);
+    if (wide) return launch_one<down_one_kernel<DT, 2, 12, 16>>(W, db * a.m, threads, down_lds, stream, a, down, db);
+    if (down <= 4) return launch_one<down_one_kernel<DT, 1, 12, 8>>(W, db * a.m, threads, down_lds, stream, a, down, db);
     return twelve_loads(DT, a.inter, 2)
-               ? launch_one<down_one_kernel<DT, 12, 8>>(W, down_blocks, threads, down_lds, stream, a, down)
-               : launch_one<down_one_kernel<DT, 16, 8>>(W, down_blocks, threads, down_lds, stream, a, down);
+               ? launch_one<down_one_kernel<DT, 2, 12, 8>>(W, db * a.m, threads, down_lds, stream, a, down, db)
+               : launch_one<down_one_kernel<DT, 2, 16, 8>>(W, db * a.m, threads, down_lds, stream, a, down, db);
+}
+
+// Each token by itself when it is the only one, or when the experts that are
+// then read more than once cost less than the map and the passes of the
+// several-token form do.  That form starts some 15 us later; at some 6.5 GB/ms
+// this is 100 MB of weights, counted for evenly spread picks.  Measured at
+// 2048 x 768 bf16 (9.4 MB an expert), top 8 of 128: 2 tokens 30.6 against
+// 41.1 us, 4 tokens 55.4 against 66, 8 tokens 103 against 102; of 8 experts
+// (every token the same): 2 tokens 29.8 against 31, 3 tokens 41.5 against 32.6.
+bool each_token(const MoeDecodeArgs& a) {
+    if (a.top_k > row_cap(a.inter)) return false;
+    if (a.m == 1) return true;
+    const double e = a.n_experts, rows = (double)a.m * a.top_k;
+    const double distinct = e * (1.0 - std::pow(1.0 - a.top_k / e, (double)a.m));
+    const double expert = 3.0 * a.hidden * a.inter * (a.dtype == kDtypeF32 ? 4 : 2);
+    return (rows - distinct) * expert < 100e6;
 }
 
 template <int DT>
 hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream) {
     const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     const uint32_t rows = a.m * a.top_k;
-    if (a.m == 1 && a.top_k <= row_cap(a.inter)) return launch_one_token<DT>(a, cus, stream);
+    if (each_token(a)) return launch_each_token<DT>(a, cus, stream);
     const uint32_t touched = few_map_ids(rows, a.n_experts);  // at most
     const uint32_t map_bytes = few_map_words(rows, a.n_experts) * 4;
     auto blocks_of = [&](uint32_t groups) {
@@ -466,7 +488,8 @@ hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream)
     if (rows <= row_cap(a.inter)) {  // every row of h fits beside the map and the output rows
         const uint32_t cols = block_columns(a.hidden, 8, cus), blocks = (a.hidden + cols - 1) / cols;
         const uint32_t lds = map_bytes + rows * 32 + staged(rows, a.inter);
-        return launch_one<down_combine_kernel<DT, 12>>(W, blocks, threads, lds, stream, a, cols);
+        return cols <= 4 ? launch_one<down_combine_kernel<DT, 1, 12>>(W, blocks, threads, lds, stream, a, cols)
+                         : launch_one<down_combine_kernel<DT, 2, 12>>(W, blocks, threads, lds, stream, a, cols);
     }
     const uint32_t blocks = blocks_of((a.hidden + 7) / 8), lds = map_bytes + staged(rows, a.inter);
     err = launch_one<down_kernel<DT, 2, 12>>(W, blocks, threads, lds, stream, a);
