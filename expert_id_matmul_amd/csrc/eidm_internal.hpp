@@ -112,7 +112,7 @@ bool moe_direct_supported(uint32_t top_k, uint32_t n_experts);
 hipError_t run_validate(const uint32_t* ids, uint32_t m, uint32_t top_k, uint32_t n_experts, int distinct,
                         hipStream_t stream, int* first_bad);
 // The expert FFN of a few tokens (moe_decode.hip); h [m*top_k][inter] and
-// y [m*top_k][hidden] are f32 scratch.
+// y [m*top_k][hidden] are f32 scratch, map the first kernel's id -> row map.
 struct MoeDecodeArgs {
     int dtype;
     uint32_t m, hidden, inter, top_k, n_experts;
@@ -120,7 +120,7 @@ struct MoeDecodeArgs {
     const uint8_t *w_gate, *w_up, *w_down;
     const float *x, *logits, *bias;
     int renormalize;
-    uint32_t* ids;
+    uint32_t *ids, *map;
     float *gates, *h, *y, *out;
 };
 hipError_t launch_moe_decode(const MoeDecodeArgs& a, int device_cus, hipStream_t stream);

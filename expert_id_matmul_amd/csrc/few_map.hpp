@@ -9,6 +9,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace eidm {
 
 struct FewMap {
@@ -40,29 +42,49 @@ __device__ __forceinline__ FewMap few_map_at(uint32_t* lds, uint32_t rows, uint3
     return f;
 }
 
-// Inclusive sum over the wavefront's lanes.
+// Inclusive sum over the wavefront's lanes: within rows of 16 by shifts, then
+// the rows' totals by broadcasts (DPP: no LDS latency).
 __device__ __forceinline__ uint32_t wave_prefix(uint32_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+    auto add = [&](auto ctrl, auto rows) {
+        v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // row_shr:2
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // row_shr:4
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // row_shr:8
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15 into rows 1, 3
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31 into rows 2, 3
     return v;
 }
 
-// The whole block takes part; ids that are >= n_ids have no list.  The map
-// is ready for every thread on return.  cost_of(rows of an id): its cost.
+constexpr uint32_t kFewMapRows = 2;   // most rows per thread
+constexpr uint32_t kFewMapUnits = 4;  // most 16-byte units per thread of a map's copy
+
+// This thread's rows' ids, requested before anything that the map is not for.
+struct FewIds {
+    uint32_t e[kFewMapRows];
+};
+
+__device__ __forceinline__ FewIds few_map_ids_load(const uint32_t* ids, uint32_t rows) {
+    FewIds f;
+#pragma unroll
+    for (uint32_t j = 0; j < kFewMapRows; ++j) f.e[j] = ids[min(threadIdx.x + j * blockDim.x, rows - 1)];
+    return f;
+}
+
+// The whole block takes part (rows <= kFewMapRows * blockDim.x); ids that are
+// >= n_ids have no list.  The map is ready for every thread on return.
+// cost_of(rows of an id): its cost.
 template <typename CostOf>
-__device__ __forceinline__ void few_map_build(const FewMap& f, const uint32_t* ids, uint32_t rows, uint32_t n_ids,
+__device__ __forceinline__ void few_map_build(const FewMap& f, const FewIds& ids, uint32_t rows, uint32_t n_ids,
                                               CostOf cost_of) {
     const uint32_t tid = threadIdx.x, nt = blockDim.x;
     for (uint32_t e = tid; e < n_ids; e += nt) f.start[e] = 0;
     __syncthreads();
-    for (uint32_t r = tid; r < rows; r += nt) {
-        const uint32_t e = ids[r];
-        if (e < n_ids) atomicAdd(&f.start[e], 1u);
-    }
+#pragma unroll
+    for (uint32_t j = 0; j < kFewMapRows; ++j)
+        if (tid + j * nt < rows && ids.e[j] < n_ids) atomicAdd(&f.start[ids.e[j]], 1u);
     __syncthreads();
     if (tid < 64) {  // one wavefront scans the counts, 64 ids at a time
         uint32_t used = 0, at = 0, spent = 0;
@@ -91,26 +113,48 @@ __device__ __forceinline__ void few_map_build(const FewMap& f, const uint32_t* i
         }
     }
     __syncthreads();
-    for (uint32_t r = tid; r < rows; r += nt) {
-        const uint32_t e = ids[r];
-        if (e < n_ids) f.row[atomicAdd(&f.start[e], 1u)] = r;
-    }
+#pragma unroll
+    for (uint32_t j = 0; j < kFewMapRows; ++j)
+        if (tid + j * nt < rows && ids.e[j] < n_ids) f.row[atomicAdd(&f.start[ids.e[j]], 1u)] = tid + j * nt;
     __syncthreads();
 }
 
+// A built map to memory, and from there into another kernel's LDS: load()
+// requests it, store() writes it (a barrier must follow).
+__device__ __forceinline__ void few_map_save(const uint32_t* lds, uint32_t words, uint32_t* to) {
+    for (uint32_t i = threadIdx.x; i < words / 4; i += blockDim.x)
+        reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<const uint4*>(lds)[i];
+}
+
+struct FewMapCopy {
+    uint4 v[kFewMapUnits];
+    __device__ __forceinline__ void load(const uint32_t* from, uint32_t words) {
+#pragma unroll
+        for (uint32_t j = 0; j < kFewMapUnits; ++j)
+            v[j] = reinterpret_cast<const uint4*>(from)[min(threadIdx.x + j * blockDim.x, words / 4 - 1)];
+    }
+    __device__ __forceinline__ void store(uint32_t* lds, uint32_t words) const {
+#pragma unroll
+        for (uint32_t j = 0; j < kFewMapUnits; ++j)
+            reinterpret_cast<uint4*>(lds)[min(threadIdx.x + j * blockDim.x, words / 4 - 1)] = v[j];
+    }
+};
+
 // The first job at or past `at` of jobs (id u, part g < parts) in order, each
 // of which costs cost[u+1] - cost[u] units, counted by part from cost[u] *
-// parts: jobs cut at such points have near equal costs.
-__device__ __forceinline__ uint32_t few_map_job(const FewMap& f, uint32_t parts, uint64_t at) {
-    uint32_t lo = 0, hi = *f.used;
-    while (lo < hi) {  // the last id that starts at or before `at`
-        const uint32_t mid = (lo + hi + 1) / 2;
-        if ((uint64_t)f.cost[mid] * parts <= at) lo = mid;
-        else hi = mid - 1;
+// parts: jobs cut at such points have near equal costs.  (At most 1024 rows of
+// 8 units and 8192 parts: 32 bits suffice.)  Every lane takes part.
+__device__ __forceinline__ uint32_t few_map_job(const FewMap& f, uint32_t parts, uint32_t at) {
+    const uint32_t used = *f.used, lane = threadIdx.x & 63;
+    uint32_t before = 0;  // ids that start at or before `at`: id 0 does
+    for (uint32_t u0 = 0; u0 < used; u0 += 64) {
+        const uint32_t u = u0 + lane;
+        before += (uint32_t)__popcll(__ballot(u < used && f.cost[min(u, used - 1)] * parts <= at));
     }
-    if (lo == *f.used) return lo * parts;
-    const uint32_t each = f.cost[lo + 1] - f.cost[lo];
-    return lo * parts + (uint32_t)((at - (uint64_t)f.cost[lo] * parts + each - 1) / each);
+    const uint32_t u = (uint32_t)__builtin_amdgcn_readfirstlane((int)before) - 1;
+    if (at >= f.cost[used] * parts) return used * parts;
+    const uint32_t each = f.cost[u + 1] - f.cost[u];
+    return u * parts + (at - f.cost[u] * parts + each - 1) / each;
 }
 
 }  // namespace eidm

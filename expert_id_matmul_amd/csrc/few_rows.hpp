@@ -16,8 +16,8 @@
 // for every four rows) the kernel spilled, and a spill's reload waits for the
 // whole ring; in LDS they cost no register and no place in the load queue.
 // Weight rows need no 16-byte alignment: the loads are declared with the
-// scalar's alignment, which global loads take at any address; only the last,
-// partial round is masked (a granule cut by k is read element-wise).
+// scalar's alignment, which global loads take at any address; the last,
+// partial round is read within the row and shifted into place.
 #pragma once
 
 #include "eidm_device.hpp"
@@ -104,6 +104,23 @@ __device__ __forceinline__ FewStage<kBatch, RowOf> few_stage(float* xs, uint32_t
     return FewStage<kBatch, RowOf>{xs, count, k, row_of, {}};
 }
 
+// Elements kk .. kk+7 of a row of k of which not all need exist (lane-varying
+// kk, wave-uniform k): where the row has 8 elements they are loaded from
+// min(kk, k - 8), so the load crosses no end and waits for no branch, and
+// few_shift() moves them into place once they have arrived.
+__device__ __forceinline__ int few_clamp(int kk, int k) { return min(kk, k - kGranule); }
+
+// w: the elements from few_clamp(kk, k) on -> those from kk on, zeros past k.
+__device__ __forceinline__ void few_shift(float (&w)[kGranule], int kk, int k) {
+    const bool cut = kk < k && kk + kGranule > k, past = kk >= k;
+    for (int s = (kGranule - k % kGranule) % kGranule; s > 0; --s) {  // the cut granule's distance, one for all lanes
+#pragma unroll
+        for (int i = 0; i < kGranule; ++i) w[i] = cut ? (i + 1 < kGranule ? w[i + 1] : 0.0f) : w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kGranule; ++i) w[i] = past ? 0.0f : w[i];
+}
+
 template <int DT>
 __device__ __forceinline__ void few_widen(const fr_u32x4 (&p)[DtypeSize<DT>::value / 2], float (&w)[kGranule]) {
     if constexpr (DT == kDtypeF32) {
@@ -146,26 +163,30 @@ struct FewStream {
             }
     }
 
-    __device__ __forceinline__ void fetch_tail(const uint8_t* const (&wrow)[C], int k) {
+    __device__ __forceinline__ void fetch_tail(Rows wrow, int k) {
         const int full = k / kRoundK;
         if (full * kRoundK == k) return;
         const int kk = full * kRoundK + slice() * kGranule;
-        tail = Slot{};
-        if (kk + kGranule <= k) {
-            fetch(wrow, full, tail);
-        } else if (kk < k) {  // a granule cut by k
+        if (k >= kGranule) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < kGranule; ++i)
-                    if (kk + i < k) {
-                        if constexpr (S == 4)
-                            tail.w[c][i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(wrow[c] + (size_t)(kk + i) * 4);
-                        else
-                            tail.w[c][0][i / 2] |=
-                                (uint32_t)*reinterpret_cast<const uint16_t*>(wrow[c] + (size_t)(kk + i) * 2) << (i % 2 * 16);
-                    }
+                for (int i = 0; i < NP; ++i)
+                    tail.w[c][i] = *reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + (size_t)few_clamp(kk, k) * S + 16 * i);
+            return;
         }
+        tail = Slot{};
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < kGranule; ++i)
+                if (kk + i < k) {
+                    if constexpr (S == 4)
+                        tail.w[c][i / 4][i % 4] = *reinterpret_cast<const uint32_t*>(wrow[c] + (size_t)(kk + i) * 4);
+                    else
+                        tail.w[c][0][i / 2] |=
+                            (uint32_t)*reinterpret_cast<const uint16_t*>(wrow[c] + (size_t)(kk + i) * 2) << (i % 2 * 16);
+                }
     }
 
     // Requests the first rounds (and the partial one) of a product.
@@ -221,7 +242,7 @@ struct FewStream {
         };
         const int last = (k + kRoundK - 1) / kRoundK - 1;
         if constexpr (kAhead) read_ahead(0);
-        auto consume = [&](int r, const Slot& s) {
+        auto consume = [&](int r, const Slot& s, bool partial = false) {
             f32x4 x[2][G];
             if constexpr (kAhead) {
 #pragma unroll
@@ -232,7 +253,10 @@ struct FewStream {
             }
             float w[C][kGranule];
 #pragma unroll
-            for (int c = 0; c < C; ++c) few_widen<DT>(s.w[c], w[c]);
+            for (int c = 0; c < C; ++c) {
+                few_widen<DT>(s.w[c], w[c]);
+                if (partial && k >= kGranule) few_shift(w[c], r * kRoundK + b * kGranule, k);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if constexpr (!kAhead) read(r, h, x[h]);
@@ -268,7 +292,7 @@ struct FewStream {
             }
         }
         if (full * kRoundK < k) {
-            consume(full, tail);
+            consume(full, tail, true);
             if constexpr (MORE) fetch_tail(next, k);
         }
     }

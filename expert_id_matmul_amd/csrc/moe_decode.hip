@@ -33,6 +33,8 @@ constexpr int kWaves = 8;  // wavefronts per block of the many-token kernels
 // (kMaxDecodeRow)
 constexpr uint32_t kRowBytes = 16 * few_row_floats(2048) * 4;
 static_assert(few_row_floats(kMaxDecodeRow) * 4 <= kRowBytes);
+static_assert(kMaxDecodeTokens * kMaxDecodeTopK <= kFewMapRows * 64 * kWaves);
+static_assert(few_map_words(kMaxDecodeTokens * kMaxDecodeTopK, kMaxExperts) <= kFewMapUnits * 4 * 64 * kWaves);
 constexpr uint32_t kRouteExperts = 256;  // experts a block routes itself (4 per lane)
 
 // most rows of k elements staged at once
@@ -155,9 +157,10 @@ __device__ __forceinline__ void expert_major(const FewMap& map, float* xs, bool 
     const uint32_t stride = few_row_floats(k);
     const uint32_t most = row_cap(k);
     const uint32_t per_expert = min(most, (uint32_t)kFewRows);
-    const uint64_t cost = (uint64_t)map.cost[*map.used] * groups;
-    uint32_t pos = few_map_job(map, groups, cost * blockIdx.x / gridDim.x);
-    const uint32_t last = few_map_job(map, groups, cost * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t cost = map.cost[*map.used] * groups, share = cost / gridDim.x, over = cost % gridDim.x;
+    uint32_t pos = few_map_job(map, groups, share * blockIdx.x + min(blockIdx.x, over));
+    const uint32_t last = few_map_job(map, groups, share * (blockIdx.x + 1) + min(blockIdx.x + 1, over));
+    pos = uniform(pos);
     while (pos < last) {  // block-uniform
         uint32_t v = pos / groups;  // experts pos/groups .. v in this pass
         const uint32_t first = map.off[v];
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_up_kernel(MoeDecodeArgs a) {
     float* xs = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));
     const bool staged = a.m <= row_cap(a.hidden);  // every token's row fits
     auto stage = few_stage<8>(xs, staged ? a.m : 0, a.hidden, [&](uint32_t t) { return a.x + (size_t)t * a.hidden; });
-    const uint32_t* ids = a.ids;
+    FewIds ids;
     if constexpr (ROUTE) {
         const uint32_t t = threadIdx.x >> 6, lane = threadIdx.x & 63;
         RouteScores<kRouteExperts / 64> sc;
@@ -254,13 +257,15 @@ __global__ __launch_bounds__(64 * kWaves) void gate_up_kernel(MoeDecodeArgs a) {
                 }
             }
         }
-        ids = picks;
         __syncthreads();
+        ids = few_map_ids_load(picks, rows);
     } else {
+        ids = few_map_ids_load(a.ids, rows);
         stage.issue();
     }
     const uint32_t most = row_cap(a.hidden);
     few_map_build(map, ids, rows, a.n_experts, [&](uint32_t r) { return job_cost(r, most); });
+    if (blockIdx.x == 0) few_map_save(lds, few_map_words(rows, a.n_experts), a.map);
     stage.finish();
     __syncthreads();
 
@@ -286,8 +291,10 @@ __global__ __launch_bounds__(64 * kWaves) void down_kernel(MoeDecodeArgs a) {
     const uint32_t rows = a.m * a.top_k;
     const FewMap map = few_map_at(lds, rows, a.n_experts);
     float* xs = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));
-    const uint32_t most = row_cap(a.inter);
-    few_map_build(map, a.ids, rows, a.n_experts, [&](uint32_t r) { return job_cost(r, most); });
+    FewMapCopy copy;  // (an expert's rows cost alike in both products but for the rows that fit in LDS)
+    copy.load(a.map, few_map_words(rows, a.n_experts));
+    copy.store(lds, few_map_words(rows, a.n_experts));
+    __syncthreads();
     const uint32_t q = threadIdx.x & 3;
     expert_major<DT, C, few_depth<DT, C>(LOADS)>(
         map, xs, false, (a.hidden + 4 * C - 1) / (4 * C), a.inter,
@@ -318,8 +325,11 @@ __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs
     float* ys = reinterpret_cast<float*>(lds + few_map_words(rows, a.n_experts));  // [rows][4*C]
     float* xs = ys + rows * 4 * C;
     auto stage = few_stage<8>(xs, rows, a.inter, [&](uint32_t r) { return a.h + (size_t)r * a.inter; });
+    FewMapCopy copy;
+    copy.load(a.map, few_map_words(rows, a.n_experts));
     stage.issue();
-    few_map_build(map, a.ids, rows, a.n_experts, [](uint32_t) { return 1u; });
+    copy.store(lds, few_map_words(rows, a.n_experts));
+    __syncthreads();
 
     const uint32_t q = threadIdx.x & 3;
     const uint32_t col0 = blockIdx.x * cols, end = min(col0 + cols, a.hidden);
@@ -514,10 +524,10 @@ hipError_t launch_moe_decode(const MoeDecodeArgs& a, int device_cus, hipStream_t
 namespace eidm {
 namespace {
 
-// scratch: h [m*top_k][inter] | y [m*top_k][hidden]
-uint64_t h_bytes(const eidm_ffn_shape* f) {
-    return ((uint64_t)f->m * f->top_k * f->inter * 4 + 255) & ~uint64_t(255);
-}
+// scratch: the id -> row map | h [m*top_k][inter] | y [m*top_k][hidden]
+uint64_t align256(uint64_t v) { return (v + 255) & ~uint64_t(255); }
+uint64_t map_bytes(const eidm_ffn_shape* f) { return align256(few_map_words(f->m * f->top_k, f->n_experts) * 4); }
+uint64_t h_bytes(const eidm_ffn_shape* f) { return align256((uint64_t)f->m * f->top_k * f->inter * 4); }
 
 eidm_shape decode_projection(const eidm_ffn_shape* f, bool down) {
     eidm_shape s{};
@@ -557,7 +567,7 @@ int decode_sizes(const eidm_ffn_shape* f, uint64_t* gate_up, uint64_t* down, uin
                         f->inter, kMaxDecodeRow);
     *gate_up = rg.required_weight_bytes;
     *down = rd.required_weight_bytes;
-    *scratch = h_bytes(f) + (uint64_t)f->m * f->top_k * f->hidden * 4;
+    *scratch = map_bytes(f) + h_bytes(f) + (uint64_t)f->m * f->top_k * f->hidden * 4;
     return EIDM_OK;
 }
 
@@ -620,8 +630,10 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
     a.renormalize = renormalize;
     a.ids = ids;
     a.gates = gates;
-    a.h = static_cast<float*>(scratch);
-    a.y = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + eidm::h_bytes(shape));
+    uint8_t* ws = static_cast<uint8_t*>(scratch);
+    a.map = reinterpret_cast<uint32_t*>(ws);
+    a.h = reinterpret_cast<float*>(ws + eidm::map_bytes(shape));
+    a.y = reinterpret_cast<float*>(ws + eidm::map_bytes(shape) + eidm::h_bytes(shape));
     a.out = out;
     const hipError_t err = eidm::launch_moe_decode(a, eidm::device_cus(), st);
     if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "decode FFN launch: %s", hipGetErrorString(err));

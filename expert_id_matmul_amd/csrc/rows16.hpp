@@ -68,17 +68,27 @@ __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT],
             t.x[u][1] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[u] + at + 4);
         }
     };
-    auto consume = [&](const Slot& t) {
-        float w[CT][kGranule];
+    auto consume = [&](const Slot& t, bool partial = false) {
+        float w[CT][kGranule], x[RT][kGranule];
+        partial = partial && k >= kGranule;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) few_widen<DT>(t.w[c], w[c]);
+        for (int c = 0; c < CT; ++c) {
+            few_widen<DT>(t.w[c], w[c]);
+            if (partial) few_shift(w[c], full * kRoundK + at0, k);
+        }
+#pragma unroll
+        for (int u = 0; u < RT; ++u) {
+#pragma unroll
+            for (int i = 0; i < kGranule; ++i) x[u][i] = t.x[u][i / 4][i % 4];
+            if (partial) few_shift(x[u], full * kRoundK + at0, k);
+        }
 #pragma unroll
         for (int i = 0; i < kGranule; ++i)
 #pragma unroll
             for (int u = 0; u < RT; ++u)
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    acc[u][c] = __builtin_amdgcn_mfma_f32_16x16x1f32(t.x[u][i / 4][i % 4], w[c][i], acc[u][c], 0, 0, 0);
+                    acc[u][c] = __builtin_amdgcn_mfma_f32_16x16x1f32(x[u][i], w[c][i], acc[u][c], 0, 0, 0);
     };
 
     Slot ring[D];
@@ -91,9 +101,19 @@ __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT],
     }
     Slot tail{};  // the partial last round: zeros past k
     const int kk = full * kRoundK + at0;
-    if (kk < k) {
-        if (kk + kGranule <= k) {
-            fetch(full, tail);
+    if (full * kRoundK < k) {
+        if (k >= kGranule) {
+            const size_t at = (size_t)few_clamp(kk, k);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    tail.w[c][i] = *reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at * S + 16 * i);
+#pragma unroll
+            for (int u = 0; u < RT; ++u) {
+                tail.x[u][0] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[u] + at);
+                tail.x[u][1] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[u] + at + 4);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kGranule; ++i)
@@ -128,7 +148,7 @@ __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT],
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (full * kRoundK < k) consume(tail);
+    if (full * kRoundK < k) consume(tail, true);
 
     // pairs (slice, slice^8), then ^4: the wavefronts; ^2, ^1: the blocks
     __syncthreads();  // xs is free
