@@ -208,10 +208,16 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _raw_stream(stream) -> int:
-    if isinstance(stream, int):
-        return stream
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# the current stream's handle without building a torch.cuda.Stream (2.5 us)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device: int) -> int:
+    if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(device)
+        stream = torch.cuda.current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _address(name: str, t, nbytes: int, device: int, dtype=None) -> int | None:
@@ -220,15 +226,16 @@ def _address(name: str, t, nbytes: int, device: int, dtype=None) -> int | None:
     device than the call's)."""
     if t is None or isinstance(t, int):
         return t  # absent, or a raw address that the caller vouches for
+    if (t.get_device() == device and t.is_contiguous() and t.nbytes >= nbytes
+            and (dtype is None or t.dtype is dtype)):
+        return t.data_ptr()
     if t.get_device() != device:
         raise ValueError(f"{name} must be a tensor of the current device ({device}), not of {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.nbytes < nbytes:
         raise ValueError(f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
 
 
 def _extent(t) -> int:
@@ -480,7 +487,7 @@ class Library:
             _address("bias", bias, 4 * shape.n_experts, dev, f32), int(renormalize),
             _id_address("ids", ids, routed, dev), _address("gates", gates, routed, dev, f32),
             _address("out", out, act, dev, f32), _address("scratch", scratch, 0, dev), _extent(scratch),
-            _raw_stream(stream))
+            _raw_stream(stream, dev))
         if rc:
             self._check(rc)
 
@@ -506,7 +513,7 @@ class Library:
             _id_address("ranks", ranks, per_adapter, dev), _address("scales", scales, per_adapter, dev, f32),
             _address("input", input, 4 * m * shape.k, dev, f32), _id_address("adapter_ids", adapter_ids, 4 * m, dev),
             _address("output", output, rows, dev, f32), _address("scratch", scratch, 0, dev), _extent(scratch),
-            _raw_stream(stream))
+            _raw_stream(stream, dev))
         if rc:
             self._check(rc)
 
