@@ -485,6 +485,8 @@ int lora_sizes(const eidm_lora_shape* f, bool shared, LoraSizes* z) {
         if (rc) return rc;
         z->weights = q.required_weight_bytes;
         z->matmul = q.scratch_bytes;
+        if (f->arith == EIDM_ARITH_SPLIT16 && dense_split16_bytes(f->m, f->k) > z->matmul)
+            z->matmul = dense_split16_bytes(f->m, f->k);
     }
     z->total = z->off_matmul + z->matmul;
     return EIDM_OK;
@@ -575,6 +577,21 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
     }
     if (weights && shape->arith == EIDM_ARITH_F32 && eidm::lora_base_few_supported(a, cus)) {
         err = eidm::launch_lora_base_few(a, shape->weight_dtype, static_cast<const uint8_t*>(weights), cus, st);
+        if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "projection launch: %s", hipGetErrorString(err));
+    } else if (weights && shape->arith == EIDM_ARITH_SPLIT16 && eidm::dense_split16_supported(a.m, a.n, cus)) {
+        err = eidm::launch_lora_shrink(a, cus, st);
+        if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter shrink launch: %s", hipGetErrorString(err));
+        eidm::MatmulArgs p{};
+        p.dtype = shape->weight_dtype;
+        p.m = a.m;
+        p.n = a.n;
+        p.k = a.k;
+        p.top_k = p.n_experts = 1;
+        p.weights = weights;
+        p.input = input;
+        p.output = output;
+        p.xsplit = reinterpret_cast<uint16_t*>(ws + z.off_matmul);
+        err = eidm::launch_dense_split16(p, cus, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "projection launch: %s", hipGetErrorString(err));
     } else {
         if (weights) a.zero_ids = reinterpret_cast<uint32_t*>(ws + z.off_ids);

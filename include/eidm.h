@@ -167,7 +167,8 @@ typedef enum eidm_kernel {
     EIDM_KERNEL_DECODE_DOWN = 19,     /* few-token FFN: down product and combine      */
     EIDM_KERNEL_LORA_SHRINK = 20,     /* adapters: v = A x                            */
     EIDM_KERNEL_LORA_EXPAND = 21,     /* adapters: y = base + scale * B v             */
-    EIDM_KERNEL_LORA_BASE = 22        /* adapters: W x of a few rows, and their shrink */
+    EIDM_KERNEL_LORA_BASE = 22,       /* adapters: W x of a few rows, and their shrink */
+    EIDM_KERNEL_DENSE_SPLIT16 = 23    /* split-16 W x of many rows with one weight     */
 } eidm_kernel;
 
 /* One kernel launch: which kernel and its launch geometry (1-D grid of

@@ -120,6 +120,39 @@ def test_split16_projection(lib, p):
     assert_close(got, run_oracle(p, d), what=p.name)
 
 
+@pytest.mark.parametrize("dtype,m,n,k", [(BF, 1300, 1500, 136), (HF, 1030, 2051, 264), (BF, 2048, 1024, 8),
+                                         (HF, 4100, 515, 1000), (BF, 130, 8200, 392), (BF, 16384, 129, 128)],
+                         ids=lambda v: str(v))
+def test_split16_projection_of_many_rows(lib, dtype, m, n, k):
+    """Sizes that fill the device with 128 x 128 tiles: every output's bits
+    against eidm_matmul_id's Direct route, with adapters on some rows."""
+    print(f"[case] {dtype} {m} {n} {k}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(k)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    tdt = torch.float16 if dtype == HF else torch.bfloat16
+    x, w = rnd(m, k), (rnd(n, k) * k ** -0.5).to(tdt)
+    a, b = rnd(2, 4, k).to(tdt), rnd(2, n, 4).to(tdt)
+    ids = torch.full((m,), -1, dtype=torch.int32, device="cuda")
+    ids[m // 2: m // 2 + 3] = 1
+    shape = B.make_lora_shape(dtype, dtype, m, n, k, 2, 4, arith=B.ARITH_SPLIT16)
+    scratch = torch.full((lib.lora_linear_scratch_bytes(shape),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = poisoned_output(m * n)
+    lib.lora_linear(shape, w, None, a, b, None, None, x, ids, out, scratch)
+    torch.cuda.synchronize()
+    assert "dense_split16" in lib.last_dispatch().kernels()
+    s = B.make_shape(dtype, m, n, k, 1, 1, n * k * 2, arith=B.ARITH_SPLIT16)
+    base, ds = torch.empty(m, n, device="cuda"), torch.empty(lib.query(s, B.DIRECT).scratch_bytes, dtype=torch.uint8, device="cuda")
+    lib.matmul_id(s, B.DIRECT, w, x, torch.zeros(m, 1, dtype=torch.int32, device="cuda"), base, ds)
+    torch.cuda.synchronize()
+    got = out[: m * n].view(m, n)
+    plain = ids < 0
+    assert torch.equal(got[plain].view(torch.int32), base[plain].view(torch.int32))
+    check_guarded(out, m * n)
+    low = (x[~plain].double() @ a[1].double().t()) @ b[1].double().t()
+    err = (got[~plain].double() - base[~plain].double() - low).abs().max() / low.abs().max()
+    assert err < 2e-5
+
+
 @pytest.mark.parametrize("given", [False, True], ids=["weights", "given"])
 @pytest.mark.parametrize("m", [7, 70, 300])
 def test_bad_ids_rank_zero_and_rows_without_an_adapter(lib, m, given):
