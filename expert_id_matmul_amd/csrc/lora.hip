@@ -2,7 +2,11 @@
 //   shrink: v[t] = A_a x[t] (max_rank numbers a row, in the library's fixed
 //     reduction order), a = the row's adapter;
 //   expand: out[t] = base[t] + scale_a * (B_a v[t]).
-// The shared projection beside them is eidm_matmul_id with one expert.
+// The shared projection beside them (base = W x), when the call computes it:
+//   * up to 3 tiles of 32 x 32 outputs a compute unit: base_few_kernel here,
+//     the F32 order;
+//   * many rows in the split-16 arithmetic: dense_split16.hip;
+//   * else eidm_matmul_id with one expert.  The same bits in each.
 //
 // An adapter is selected per row as an expert is (mlx-native 0.13.0,
 // src/ops/dense_matmul_id_auto.rs: a stack of weights, one id per row).
@@ -13,6 +17,12 @@
 // sorted by adapter (the library's id -> row map) and 16 rows of one adapter
 // read it once.  A decode batch's shared projection and its shrink
 // run side by side in one launch.
+//
+// Bounds.  The shrink and expand are far below the matrix rate; the expand
+// moves the base rows in and the results out (16384 x 2048: 268 MB, 55 us,
+// 4.9 TB/s), the shrink the rows of x.  A few rows' projection is bound by
+// what a compute unit's cache takes in of misses, x and W in f32 and 16 bits
+// (32 x 1536 x 4096: 18 us; the products alone would take 3.5).
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
@@ -36,36 +46,52 @@ __device__ __forceinline__ void write_zero_ids(const LoraArgs& a) {
             a.zero_ids[i] = 0;
 }
 
-// Work of one block of 256: ranks 16*part .. of row t, four per wavefront;
-// the row is staged in LDS.
+// Work of one block of 256 of the `blocks` that share row t: wavefront w takes
+// the groups of four ranks block + blocks * (w, w + 4, ...); the row is staged
+// in LDS.
 template <int DT>
-__device__ __forceinline__ void shrink_row(const LoraArgs& a, uint32_t t, uint32_t part, float* xs) {
+__device__ __forceinline__ void shrink_row(const LoraArgs& a, uint32_t t, uint32_t block, uint32_t blocks, float* xs) {
     const uint32_t q = threadIdx.x & 3;
     const uint32_t id = a.ids[t];
     if (id >= a.n_adapters) return;
     const uint32_t rank = rank_of(a, id);
-    if (part * 16 >= rank) return;
-    const uint32_t i0 = part * 16 + (threadIdx.x >> 6) * 4;
-    const uint8_t* const wrow[1] = {a.a + (size_t)id * a.a_stride +
-                                    (size_t)min(i0 + q, rank - 1) * a.k * DtypeSize<DT>::value};
+    if (block * 4 >= rank) return;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const uint32_t step = 16 * blocks;  // ranks between a wavefront's groups
+    uint32_t i0 = 4 * (block + blocks * wave);
+    auto weights_at = [&](uint32_t i, const uint8_t* (&to)[1]) {
+        to[0] = a.a + (size_t)id * a.a_stride + (size_t)min(i + q, rank - 1) * a.k * DtypeSize<DT>::value;
+    };
+    const uint8_t* wrow[1];
+    weights_at(i0, wrow);
     FewStream<DT, 1, DtypeSize<DT>::value == 4 ? 4 : 8, false> w;
     auto stage = few_stage<8>(xs, 1, a.k, [&](uint32_t) { return a.x + (size_t)t * a.k; });
     stage.issue();  // ahead of the weights: a thread's loads return in order
     w.start(wrow, (int)a.k);  // in every wavefront: behind a branch, the rows' wait would be for the weights too
     stage.finish();
     __syncthreads();
-    if (i0 >= rank) return;
-    few_rows_tile<0, false>(w, wrow, wrow, xs, 0, 1, (int)a.k, [](uint32_t) { return 0; },
-                            [&](uint32_t, const float (&v)[1]) {
-                                if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
-                            });
+    while (i0 < rank) {  // wave-uniform
+        auto emit = [&](uint32_t, const float (&v)[1]) {
+            if (i0 + q < rank) a.v[(size_t)t * a.v_stride + i0 + q] = v[0];
+        };
+        auto row = [](uint32_t) { return 0; };
+        const uint8_t* next[1] = {wrow[0]};
+        if (i0 + step < rank) {
+            weights_at(i0 + step, next);
+            few_rows_tile<0, true>(w, wrow, next, xs, 0, 1, (int)a.k, row, emit);
+            wrow[0] = next[0];
+        } else {
+            few_rows_tile<0, false>(w, wrow, next, xs, 0, 1, (int)a.k, row, emit);
+        }
+        i0 += step;
+    }
 }
 
 template <int DT>
 __global__ __launch_bounds__(256) void shrink_row_kernel(LoraArgs a, uint32_t parts) {
     extern __shared__ __align__(16) float xs[];
     write_zero_ids(a);
-    shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, xs);
+    shrink_row<DT>(a, blockIdx.x / parts, blockIdx.x % parts, parts, xs);
 }
 
 // The shared projection (a.out = W x) and, in the last `shrinks` blocks of
@@ -78,7 +104,7 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
     extern __shared__ __align__(16) float xs[];
     const uint32_t block = blockIdx.x, bases = gridDim.x - shrinks, lane = threadIdx.x & 63;
     if (block >= bases) {
-        shrink_row<DT>(a, (block - bases) / parts, (block - bases) % parts, xs);
+        shrink_row<DT>(a, (block - bases) / parts, (block - bases) % parts, parts, xs);
         return;
     }
     if constexpr (CT == 0) {
@@ -306,12 +332,23 @@ hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
     return launched(EIDM_KERNEL_LORA_SHRINK, grid, 256, 0);
 }
 
+// Blocks per row of a shrink beside `bases` blocks of the projection.  A
+// compute unit left to the shrink alone does not delay a tile, so the rows
+// share those that the tiles leave; without enough of them a few rows take a
+// block per four ranks, which adds least to each tile it runs beside, and
+// more rows one per 16 (each block stages its row).
+uint32_t shrink_parts(const LoraArgs& a, uint32_t bases, uint32_t cus) {
+    const uint32_t groups = (a.max_rank + 3) / 4, left = bases < cus ? (cus - bases) / a.m : 0;
+    if (left) return groups < left ? groups : left;
+    return a.m <= 4 ? groups : (groups + 3) / 4;
+}
+
 template <int DT, int RT, int CT>
-hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, hipStream_t stream) {
-    const uint32_t parts = (a.max_rank + 15) / 16, shrinks = with_shrink ? a.m * parts : 0;
+hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, uint32_t cus, hipStream_t stream) {
     constexpr uint32_t C = CT ? 16 * CT : 16, R = CT ? 16 * RT : 1;
     const uint32_t ctiles = (a.n + C - 1) / C, rtiles = (a.m + R - 1) / R;
     const uint32_t blocks = CT ? (ctiles + 7) / 8 * 8 * rtiles : ctiles;
+    const uint32_t parts = shrink_parts(a, ctiles * rtiles, cus), shrinks = with_shrink ? a.m * parts : 0;
     uint32_t lds = CT ? rows16_lds(RT * CT) * 4 : a.m * few_row_floats(a.k) * 4;
     if (with_shrink && lds < few_row_floats(a.k) * 4) lds = few_row_floats(a.k) * 4;
     hipLaunchKernelGGL((base_few_kernel<DT, RT, CT>), dim3(shrinks + blocks), dim3(256), lds, stream, a, weights,
@@ -328,17 +365,17 @@ uint64_t makespan(const LoraArgs& a, uint32_t rt, uint32_t ct, uint32_t each, ui
 
 template <int DT>
 hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, int device_cus, hipStream_t stream) {
+    const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     if (a.m <= 4 && stages_rows(a.m, a.k))
-        return a.m == 1 ? base_few<DT, 0, 0>(a, weights, with_shrink, stream)
-                        : base_few<DT, 1, 0>(a, weights, with_shrink, stream);
+        return a.m == 1 ? base_few<DT, 0, 0>(a, weights, with_shrink, cus, stream)
+                        : base_few<DT, 1, 0>(a, weights, with_shrink, cus, stream);
     // larger tiles read less per product, smaller ones spread more evenly; one
     // tile of each kind per compute unit takes 12, 17 and 23.5 us at k = 4096
     // (6, 9 and 13 at k = 2048)
-    const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     const uint64_t one = makespan(a, 1, 1, 24, cus), two = makespan(a, 1, 2, 34, cus), four = makespan(a, 2, 2, 48, cus);
-    if (one <= two && one <= four) return base_few<DT, 1, 1>(a, weights, with_shrink, stream);
-    return two <= four ? base_few<DT, 1, 2>(a, weights, with_shrink, stream)
-                       : base_few<DT, 2, 2>(a, weights, with_shrink, stream);
+    if (one <= two && one <= four) return base_few<DT, 1, 1>(a, weights, with_shrink, cus, stream);
+    return two <= four ? base_few<DT, 1, 2>(a, weights, with_shrink, cus, stream)
+                       : base_few<DT, 2, 2>(a, weights, with_shrink, cus, stream);
 }
 
 template <int DT>

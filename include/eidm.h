@@ -420,13 +420,18 @@ int eidm_moe_ffn(const eidm_ffn_shape* shape, int route, const void* w_gate, con
  * The expert FFN of a few tokens (a decode step of up to
  * EIDM_DECODE_MAX_TOKENS requests): the computation, the arguments and the
  * bits of eidm_moe_ffn, reading each touched expert's three matrices once
- * however many of the tokens chose it, in one launch for routing, gate, up
- * and silu * up, and one for down and combine.
- * Requires m <= EIDM_DECODE_MAX_TOKENS, top_k <= 16 and the router's limits
- * (else EIDM_E_UNSUPPORTED).  Weights need the scalar's alignment only; no
- * buffer may overlap another.  scratch: device, 256-byte aligned, at least
- * eidm_moe_ffn_decode_scratch_bytes(shape) bytes; its contents need no
- * preparation and mean nothing afterwards.
+ * for up to 16 of the rows that chose it.  A token by itself, and a few that
+ * share hardly any expert, take two launches (routing, gate, up and
+ * silu * up; down and combine); other calls share the experts' reads between
+ * tokens, with a launch of their own for routing (m > 8 or n_experts > 256)
+ * and for combine (rows of h beyond a block's LDS).  Every form has the same
+ * bits, and a token's results depend on no other token.
+ * Requires m <= EIDM_DECODE_MAX_TOKENS, top_k <= 16, hidden and inter <=
+ * 32768 and the router's limits (else EIDM_E_UNSUPPORTED).  Weights need the
+ * scalar's alignment only; no buffer may overlap another.  scratch: device,
+ * 256-byte aligned, at least eidm_moe_ffn_decode_scratch_bytes(shape) bytes;
+ * its contents need no preparation and mean nothing afterwards, and calls
+ * that may overlap in time need one each.
  */
 uint64_t eidm_moe_ffn_decode_scratch_bytes(const eidm_ffn_shape* shape);
 
@@ -470,16 +475,20 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
  *               other id >= n_adapters makes the row quiet NaN.
  * output        device f32 [m, n]; overlaps nothing but, whole, base
  * scratch       device, 256-byte aligned, at least
- *               eidm_lora_linear_scratch_bytes(shape) bytes; its contents
- *               need no preparation and mean nothing afterwards
- * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m and n*... as
- * for eidm_matmul_id (else EIDM_E_UNSUPPORTED).
+ *               eidm_lora_linear_scratch_bytes(shape) bytes (which count the
+ *               shared projection's; the shape's weight_dtype and arith must
+ *               be valid for that call); its contents need no preparation
+ *               and mean nothing afterwards, and calls that may overlap in
+ *               time need one each
+ * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m, n and k as
+ * for eidm_matmul_id, and a launch's grid: (m / 16 + n_adapters + 1) *
+ * ceil(n / 256) < 2^31 (else EIDM_E_UNSUPPORTED).
  */
 typedef struct eidm_lora_shape {
     uint32_t struct_size;    /* sizeof(eidm_lora_shape) */
     int32_t weight_dtype;    /* eidm_dtype of W (not read when base is given) */
     int32_t adapter_dtype;   /* eidm_dtype of A and B   */
-    int32_t arith;           /* eidm_arith of W x       */
+    int32_t arith;           /* eidm_arith of W x (not read when base is given) */
     uint32_t m, n, k;        /* rows, output columns, reduction length */
     uint32_t n_adapters, max_rank, reserved0;
     uint64_t a_stride_bytes; /* bytes between adapters of A */

@@ -153,6 +153,39 @@ def test_split16_projection_of_many_rows(lib, dtype, m, n, k):
     assert err < 2e-5
 
 
+@pytest.mark.parametrize("dtype", [HF, BF], ids=["f16", "bf16"])
+def test_split16_projection_of_many_rows_with_special_values(lib, dtype):
+    """Infinite, NaN, subnormal and (for f16) out-of-range activations: the
+    same values as eidm_matmul_id's Direct route, and other rows untouched."""
+    m, n, k = 1100, 1920, 72
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(m, k, generator=g, device="cuda")
+    tdt = torch.float16 if dtype == HF else torch.bfloat16
+    w = (torch.randn(n, k, generator=g, device="cuda") * 0.1).to(tdt)
+    clean = x.clone()
+    x[3, 5], x[130, 71], x[131, 0], x[1099, 8] = float("inf"), float("nan"), -float("inf"), 1e6
+    x[700], x[701, 3] = 1e-42, 3.4e38
+    odd = [3, 130, 131, 700, 701, 1099]
+    a, b = torch.zeros(1, 2, k, device="cuda", dtype=tdt), torch.zeros(1, n, 2, device="cuda", dtype=tdt)
+    ids = torch.full((m,), -1, dtype=torch.int32, device="cuda")
+    shape = B.make_lora_shape(dtype, dtype, m, n, k, 1, 2, arith=B.ARITH_SPLIT16)
+    scratch = torch.full((lib.lora_linear_scratch_bytes(shape),), 0xFF, dtype=torch.uint8, device="cuda")
+    out, plain = (torch.empty(m, n, device="cuda") for _ in range(2))
+    lib.lora_linear(shape, w, None, a, b, None, None, x, ids, out, scratch)
+    assert "dense_split16" in lib.last_dispatch().kernels()
+    lib.lora_linear(shape, w, None, a, b, None, None, clean, ids, plain, scratch)
+    s = B.make_shape(dtype, m, n, k, 1, 1, n * k * 2, arith=B.ARITH_SPLIT16)
+    want, ds = torch.empty(m, n, device="cuda"), torch.empty(lib.query(s, B.DIRECT).scratch_bytes, dtype=torch.uint8, device="cuda")
+    lib.matmul_id(s, B.DIRECT, w, x, torch.zeros(m, 1, dtype=torch.int32, device="cuda"), want, ds)
+    torch.cuda.synchronize()
+    nan = want.isnan()
+    assert nan.any() and torch.equal(nan, out.isnan())
+    assert torch.equal(out[~nan].view(torch.int32), want[~nan].view(torch.int32))
+    same = torch.ones(m, dtype=torch.bool, device="cuda")
+    same[odd] = False
+    assert torch.equal(out[same].view(torch.int32), plain[same].view(torch.int32))
+
+
 @pytest.mark.parametrize("given", [False, True], ids=["weights", "given"])
 @pytest.mark.parametrize("m", [7, 70, 300])
 def test_bad_ids_rank_zero_and_rows_without_an_adapter(lib, m, given):
@@ -230,6 +263,7 @@ def test_buffers_at_the_scalar_alignment(lib, m, dtype):
                                Lora("graph_one", BF, BF, 1, 256, 512, 8, 16, none=0.0),
                                Lora("graph_prompts", BF, BF, 400, 256, 512, 8, 16, runs=5),
                                Lora("graph_split", BF, BF, 200, 256, 512, 8, 16, runs=5, arith=1),
+                               Lora("graph_dense_split", BF, BF, 1024, 2048, 136, 8, 16, runs=5, arith=1),
                                Lora("graph_given", BF, BF, 300, 256, 512, 8, 16, given=True)], ids=lambda p: p.name)
 def test_graph_replays_match_eager(lib, p):
     print(f"[case] {p.name}", flush=True)

@@ -60,6 +60,15 @@ def test_decode_refuses_more_slots_than_its_limit(lib):
     assert decode(lib, ffn(n_experts=64, top_k=17), gu=1 << 30, dn=1 << 30)[0] == B.E_UNSUPPORTED
 
 
+@pytest.mark.parametrize("hidden,inter,code", [(32768, 8, 0), (8, 32768, 0), (32769, 8, B.E_UNSUPPORTED),
+                                               (8, 32769, B.E_UNSUPPORTED)])
+def test_decode_limits_the_length_of_a_row(lib, hidden, inter, code):
+    s = B.make_ffn_shape(B.BF16, 3, hidden, inter, 2, 4)
+    if code:
+        assert decode(lib, s, gu=1 << 40, dn=1 << 40)[0] == code
+    assert (lib.lib.eidm_moe_ffn_decode_scratch_bytes(ctypes.byref(s)) == 0) == (code != 0)
+
+
 @pytest.mark.parametrize("arg", ["w_gate", "w_up", "w_down", "x", "logits", "ids", "gates", "out", "scratch"])
 def test_decode_refuses_null_buffers(lib, arg):
     assert decode(lib, ffn(), **{arg: None})[0] == B.E_INVALID
@@ -116,6 +125,16 @@ def test_lora_refuses_bad_shapes(lib, field, value, code):
 def test_lora_refuses_ranks_above_its_limit(lib):
     s = B.make_lora_shape(B.BF16, B.BF16, 6, 48, 64, 4, 257)
     assert linear(lib, s, abytes=1 << 30, bbytes=1 << 30) == B.E_UNSUPPORTED
+
+
+def test_lora_refuses_a_grid_beyond_a_launch(lib):
+    s = B.make_lora_shape(B.BF16, B.BF16, 1 << 26, 1 << 18, 8, 4, 8)
+    assert linear(lib, s, abytes=1 << 40, bbytes=1 << 40, wbytes=1 << 40) == B.E_UNSUPPORTED
+
+
+def test_lora_reads_no_weight_dtype_beside_a_base(lib):
+    s = lora(weight_dtype=77, arith=5)
+    assert linear(lib, s, w=None, base=FAKE, sbytes=255) == B.E_SIZE  # past the shape's checks
 
 
 def test_lora_takes_weights_or_base_and_not_both(lib):
