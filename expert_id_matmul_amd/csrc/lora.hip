@@ -214,6 +214,8 @@ __device__ __forceinline__ void load_b(const uint8_t* row, uint32_t i0, uint32_t
 }
 
 // One thread per output: the row's adapter alone, 32 ranks' loads at once.
+// Latency bound (id, then B, then the sums): the first loads do not wait for
+// the row's rank, so up to 32 ranks they may take elements past it.
 template <int DT>
 __global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
     constexpr uint32_t kBatch = 4;
@@ -225,20 +227,34 @@ __global__ __launch_bounds__(256) void expand_row_kernel(LoraArgs a) {
         const uint32_t id = a.ids[t];
         float y = a.base[t * a.n + j];
         if (id < a.n_adapters) {
-            const uint32_t rank = rank_of(a, id);
             const uint8_t* row = a.b + (size_t)id * a.b_stride + (size_t)j * a.max_rank * DtypeSize<DT>::value;
+            float b[kBatch][kGranule];
+            auto load = [&](uint32_t i0) {
+#pragma unroll
+                for (uint32_t h = 0; h < kBatch; ++h)
+                    if (i0 + h * kGranule < a.max_rank) load_b<DT>(row, i0 + h * kGranule, a.max_rank, b[h]);
+            };
+            load(0);
+            const uint32_t rank = rank_of(a, id);
             const float* v = a.v + t * a.v_stride;
             float u = 0.0f;
-            for (uint32_t i0 = 0; i0 < rank; i0 += kBatch * kGranule) {
-                float b[kBatch][kGranule];
+            for (uint32_t i0 = 0; i0 < rank;) {
 #pragma unroll
-                for (uint32_t h = 0; h < kBatch; ++h)
-                    if (i0 + h * kGranule < rank) load_b<DT>(row, i0 + h * kGranule, a.max_rank, b[h]);
+                for (uint32_t h = 0; h < kBatch; ++h) {
+                    const float* vh = v + i0 + h * kGranule;
+                    if (i0 + (h + 1) * kGranule <= rank) {
 #pragma unroll
-                for (uint32_t h = 0; h < kBatch; ++h)
+                        for (uint32_t i = 0; i < kGranule; ++i) u = fma_step(vh[i], b[h][i], u);
+                    } else {  // the granule that the rank ends in
+                        for (uint32_t i = 0; i0 + h * kGranule + i < rank; ++i) {
+                            u = fma_step(vh[i], b[h][0], u);
 #pragma unroll
-                    for (uint32_t i = 0; i < kGranule; ++i)
-                        if (i0 + h * kGranule + i < rank) u = fma_step(v[i0 + h * kGranule + i], b[h][i], u);
+                            for (uint32_t e = 0; e + 1 < kGranule; ++e) b[h][e] = b[h][e + 1];
+                        }
+                    }
+                }
+                i0 += kBatch * kGranule;
+                if (i0 < rank) load(i0);
             }
             if (rank) y = fma_step(scale_of(a, id), u, y);
         } else if (id != EIDM_NO_ADAPTER) {
