@@ -100,6 +100,14 @@ __global__ __launch_bounds__(256) void pack_split16_kernel(const float* __restri
     }
 }
 
+// A column's chunks stand xor-ed with 0, 2, 3, 1 by its four-column group: the
+// 16 columns of one chunk fall on all 64 banks, and so do 8 columns each of
+// two neighbouring chunks, in which the 16-byte reads are served.
+__device__ __forceinline__ uint32_t place(uint32_t col) {
+    const uint32_t a = col >> 2 & 3;
+    return a >> 1 | ((a ^ a >> 1) & 1) << 1;
+}
+
 // group_rows x group_cols tiles form one XCD's group.
 template <int DT>
 __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __restrict__ packed,
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
         const uint32_t c0 = pair * 8 + whalf * 4;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c)
-            buf[b][whalf][wcol][c ^ (wcol >> 2 & 3)] = c0 + c < chunks ? w[c] : ds_u32x4{0, 0, 0, 0};  // zeros past k
+            buf[b][whalf][wcol][c ^ place(wcol)] = c0 + c < chunks ? w[c] : ds_u32x4{0, 0, 0, 0};  // zeros past k
     };
 
     f32x4 hi[kWaveRows][kColTiles], lo[kWaveRows][kColTiles];
@@ -178,7 +186,7 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
             for (int h = 0; h < kColTiles; h += 4) {
                 ds_u32x4 wt[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) wt[c] = buf[b][h2][(h + c) * 16 + i][g ^ (i >> 2 & 3)];
+                for (int c = 0; c < 4; ++c) wt[c] = buf[b][h2][(h + c) * 16 + i][g ^ place(i)];
 #pragma unroll
                 for (int t = 0; t < kWaveRows; ++t)
 #pragma unroll
