@@ -15,14 +15,15 @@
 //     buffer, two buffers, one barrier per 96 products a wavefront.  A
 //     column's four 16-byte chunks are stored permuted by its index, so the
 //     16 columns that are read together fall on all banks.
-// LDS then carries 40 KB per 32 of k for 192 matrix instructions, well under
-// what they take; with both operands in LDS it was the bound.
+// LDS then carries 40 KB per 32 of k (some 320 cycles) beside the 768 cycles
+// of a wavefront's 48 matrix instructions; with the rows there too it would be
+// 88 KB, as long as the products.
 // Blocks run in groups of up to 64 tiles per XCD, near square, whose operands
 // its L2 serves; fewer tiles make smaller groups, so that all XCDs have one
 // (1024 x 4096 x 4096: 133 us, 189 with groups of 64 on half of them).
-// Measured at 2048 x 4096 x 4096, bf16: 182 us, 1.13 PFLOP/s of 16-bit products
-// (a large library product in bf16 reaches the same rate), and 16 us for the
-// split.
+// Measured at 2048 x 4096 x 4096, bf16: 177-185 us, 1.11-1.16 PFLOP/s of 16-bit
+// products (a large library product in bf16 reaches the same rate), and 16 us
+// for the split.
 //
 // mlx-native 0.13.0, src/ops/dense_matmul_id_auto.rs: the value-independence
 // theorem statement (one order, whichever rows are computed together).

@@ -18,11 +18,14 @@
 // read it once.  A decode batch's shared projection and its shrink
 // run side by side in one launch.
 //
-// Bounds.  The shrink and expand are far below the matrix rate; the expand
-// moves the base rows in and the results out (16384 x 2048: 268 MB, 55 us,
-// 4.9 TB/s), the shrink the rows of x.  A few rows' projection is bound by
-// what a compute unit's cache takes in of misses, x and W in f32 and 16 bits
-// (32 x 1536 x 4096: 18 us; the products alone would take 3.5).
+// Bounds.  By tiles the expand is a copy with a few products: the base rows
+// in, the results out (16384 x 2048, 268 MB: 62 us, 4.3 TB/s, a copy's rate);
+// the shrink reads the rows of x (16384 x 768: 16.5 us).  A few rows'
+// projection is bound by what a compute unit takes in through its first-level
+// cache, f32 rows and 16-bit weights: 32 x 1536 x 4096 moves 393 KB per unit in
+// 12 us, the products alone would take 3.5 (with the shrink beside it 14.8 us,
+// the expand 5.4).  One row of 4096 x 4096: 34 MB in 9.6 us (3.5 TB/s), two
+// thirds of it the stream, the rest its start and end.
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"

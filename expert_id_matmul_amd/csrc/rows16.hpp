@@ -22,7 +22,6 @@ namespace eidm {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTileRows = 16;
 constexpr int kTileWaves = 4;
 
 // LDS floats of rows16_product
