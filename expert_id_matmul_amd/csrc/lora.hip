@@ -26,6 +26,8 @@
 // 12 us, the products alone would take 3.5 (with the shrink beside it 14.8 us,
 // the expand 5.4).  One row of 4096 x 4096: 34 MB in 9.6 us (3.5 TB/s), two
 // thirds of it the stream, the rest its start and end.
+#include <algorithm>
+
 #include "eidm.h"
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
@@ -139,7 +141,7 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
 #pragma unroll
         for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(row0 + t * 16 + i, a.m - 1) * a.k;
         float total[RT][CT];
-        rows16_product<DT, RT, CT, RT * CT == 1 ? 8 : RT * CT == 2 ? 6 : 4, false>(wrow, xrow, (int)a.k, xs, total);
+        rows16_product<DT, RT, CT, RT * CT <= 2 ? 4 : 2, false>(wrow, xrow, (int)a.k, xs, total);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const uint32_t r = row0 + t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(256, 5 - CT - (DT == kDtypeF32)) void shrink_tile_k
     for (uint32_t c = 0; c < CT; ++c)
         wrow[c] = a.a + (size_t)t.id * a.a_stride + (size_t)min(c0 + 16 * c + i, rank - 1) * a.k * DtypeSize<DT>::value;
     float total[1][CT];
-    rows16_product<DT, 1, CT, 6, false>(wrow, xrow, (int)a.k, xs, total);
+    rows16_product<DT, 1, CT, 4, false>(wrow, xrow, (int)a.k, xs, total);
     const uint32_t r = 4 * (lane >> 4) + (threadIdx.x >> 6);
     const uint32_t to = (uint32_t)__shfl((int)row, (int)r);
 #pragma unroll
@@ -403,12 +405,14 @@ hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shri
         return a.m == 1 ? base_few<DT, 0, 0>(a, weights, with_shrink, cus, stream)
                         : base_few<DT, 1, 0>(a, weights, with_shrink, cus, stream);
     // larger tiles read less per product, smaller ones spread more evenly; one
-    // tile of each kind per compute unit takes 12, 17 and 23.5 us at k = 4096
-    // (6, 9 and 13 at k = 2048)
-    const uint64_t one = makespan(a, 1, 1, 24, cus), two = makespan(a, 1, 2, 34, cus), four = makespan(a, 2, 2, 48, cus);
-    if (one <= two && one <= four) return base_few<DT, 1, 1>(a, weights, with_shrink, cus, stream);
-    return two <= four ? base_few<DT, 1, 2>(a, weights, with_shrink, cus, stream)
-                       : base_few<DT, 2, 2>(a, weights, with_shrink, cus, stream);
+    // tile of each kind per compute unit takes 13, 17, 24 and 32 us at k = 4096
+    const uint64_t one = makespan(a, 1, 1, 13, cus), two = makespan(a, 1, 2, 17, cus), four = makespan(a, 2, 2, 24, cus),
+                   six = makespan(a, 2, 3, 32, cus);
+    const uint64_t least = std::min({one, two, four, six});
+    if (one == least) return base_few<DT, 1, 1>(a, weights, with_shrink, cus, stream);
+    if (two == least) return base_few<DT, 1, 2>(a, weights, with_shrink, cus, stream);
+    return four == least ? base_few<DT, 2, 2>(a, weights, with_shrink, cus, stream)
+                         : base_few<DT, 2, 3>(a, weights, with_shrink, cus, stream);
 }
 
 template <int DT>

@@ -24,9 +24,17 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTileWaves = 4;
 
+// Tiles whose sums meet in LDS at once: up to four (64 KB), else half of them.
+constexpr int rows16_part(int tiles) { return tiles > 4 ? tiles / 2 : tiles; }
 // LDS floats of rows16_product
-constexpr uint32_t rows16_lds(int tiles) { return (uint32_t)tiles * kTileWaves * 16 * 64; }
+constexpr uint32_t rows16_lds(int tiles) { return (uint32_t)rows16_part(tiles) * kTileWaves * 16 * 64; }
 
+// D rounds are in flight, 4 for up to two tiles and 2 beyond: what a unit's
+// cache holds of misses bounds the loads, and more rounds than that only push
+// its lines out (64 x 1536 x 4096 bf16, two tiles: 20.1 us with 4, 20.9 with 6,
+// 20.9 with 8, 24.3 with 2; 512 x 1024 x 2048, four tiles: 29.9 with 2, 31.0
+// with 4, 34.9 with 6).
+//
 // wrow[c]: this lane's weight row (row l%16 of column tile c), xrow[t]: its
 // activation row of row tile t; lanes without one repeat a valid row.  On
 // return total[t][c] of lane l of wavefront v is (row 4*(l/16)+v of tile t,
@@ -150,26 +158,29 @@ __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT],
     if (full * kRoundK < k) consume(tail, true);
 
     // pairs (slice, slice^8), then ^4: the wavefronts; ^2, ^1: the blocks
-    __syncthreads();  // xs is free
-    constexpr int T = RT * CT;
-    f32x4* mine = reinterpret_cast<f32x4*>(xs) + (size_t)j * T * 4 * 64 + lane;
+    constexpr int T = RT * CT, P = rows16_part(T);
 #pragma unroll
-    for (int t = 0; t < T; ++t)
+    for (int t0 = 0; t0 < T; t0 += P) {
+        __syncthreads();  // xs is free
+        f32x4* mine = reinterpret_cast<f32x4*>(xs) + (size_t)j * P * 4 * 64 + lane;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {  // the four blocks' sums of one output together
-            const f32x16& e = acc[t / CT][t % CT];
-            mine[(t * 4 + v) * 64] = f32x4{e[v], e[4 + v], e[8 + v], e[12 + v]};
+        for (int t = 0; t < P; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {  // the four blocks' sums of one output together
+                const f32x16& e = acc[(t0 + t) / CT][(t0 + t) % CT];
+                mine[(t * 4 + v) * 64] = f32x4{e[v], e[4 + v], e[8 + v], e[12 + v]};
+            }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < P; ++t) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(xs) + (t * 4 + j) * 64 + lane;
+            constexpr int W = P * 4 * 64;
+            const f32x4 a = p[0], b = p[W], c = p[2 * W], d = p[3 * W];
+            f32x4 q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = (a[i] + c[i]) + (b[i] + d[i]);
+            total[(t0 + t) / CT][(t0 + t) % CT] = (q[0] + q[2]) + (q[1] + q[3]);
         }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-        const f32x4* p = reinterpret_cast<const f32x4*>(xs) + (t * 4 + j) * 64 + lane;
-        constexpr int W = T * 4 * 64;
-        const f32x4 a = p[0], b = p[W], c = p[2 * W], d = p[3 * W];
-        f32x4 q;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = (a[i] + c[i]) + (b[i] + d[i]);
-        total[t / CT][t % CT] = (q[0] + q[2]) + (q[1] + q[3]);
     }
 }
 

@@ -98,6 +98,30 @@ def test_every_batch_size(lib, m):
     same_bits(alone[0], got[t])
 
 
+@pytest.mark.parametrize("dtype,m,n,k", [(BF, 500, 750, 136), (HF, 512, 768, 131), (FL, 481, 737, 200), (BF, 97, 2000, 264),
+                                         (HF, 130, 1500, 72), (FL, 60, 1530, 140)], ids=lambda v: str(v))
+def test_projection_tiles_of_every_size(lib, dtype, m, n, k):
+    """16 x 16 to 32 x 48 outputs a block, whole and cut: the bits of
+    eidm_matmul_id's Direct route."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    tdt = {HF: torch.float16, BF: torch.bfloat16, FL: torch.float32}[dtype]
+    x = torch.randn(m, k, generator=g, device="cuda")
+    w = (torch.randn(n, k, generator=g, device="cuda") * k ** -0.5).to(tdt)
+    a, b = torch.zeros(1, 4, k, device="cuda", dtype=tdt), torch.zeros(1, n, 4, device="cuda", dtype=tdt)
+    ids = torch.full((m,), -1, dtype=torch.int32, device="cuda")
+    shape = B.make_lora_shape(dtype, dtype, m, n, k, 1, 4)
+    scratch = torch.full((lib.lora_linear_scratch_bytes(shape),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = poisoned_output(m * n)
+    lib.lora_linear(shape, w, None, a, b, None, None, x, ids, out, scratch)
+    assert "lora_base" in lib.last_dispatch().kernels()
+    want = torch.empty(m, n, device="cuda")
+    s = B.make_shape(dtype, m, n, k, 1, 1, n * k * W.DTYPE_SIZE[dtype])
+    lib.matmul_id(s, B.DIRECT, w, x, torch.zeros(m, 1, dtype=torch.int32, device="cuda"), want)
+    torch.cuda.synchronize()
+    check_guarded(out, m * n)
+    assert torch.equal(out[: m * n].view(m, n).view(torch.int32), want.view(torch.int32))
+
+
 @pytest.mark.parametrize("p", [Lora("split_bf16", BF, BF, 40, 128, 256, 6, 16, arith=1),
                                Lora("split_one", BF, BF, 1, 272, 520, 4, 8, arith=1),
                                Lora("split_f16", HF, HF, 300, 144, 264, 5, 24, runs=4, arith=1),
