@@ -141,7 +141,7 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
 #pragma unroll
         for (int t = 0; t < RT; ++t) xrow[t] = a.x + (size_t)min(row0 + t * 16 + i, a.m - 1) * a.k;
         float total[RT][CT];
-        rows16_product<DT, RT, CT, RT * CT <= 2 ? 4 : 2, false>(wrow, xrow, (int)a.k, xs, total);
+        rows16_product<DT, RT, CT, RT * CT <= 2 ? 4 : 2>(wrow, xrow, (int)a.k, xs, total);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const uint32_t r = row0 + t * 16 + 4 * (lane >> 4) + (threadIdx.x >> 6);
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(256, 5 - CT - (DT == kDtypeF32)) void shrink_tile_k
     for (uint32_t c = 0; c < CT; ++c)
         wrow[c] = a.a + (size_t)t.id * a.a_stride + (size_t)min(c0 + 16 * c + i, rank - 1) * a.k * DtypeSize<DT>::value;
     float total[1][CT];
-    rows16_product<DT, 1, CT, 4, false>(wrow, xrow, (int)a.k, xs, total);
+    rows16_product<DT, 1, CT, 4>(wrow, xrow, (int)a.k, xs, total);
     const uint32_t r = 4 * (lane >> 4) + (threadIdx.x >> 6);
     const uint32_t to = (uint32_t)__shfl((int)row, (int)r);
 #pragma unroll

@@ -8,7 +8,8 @@
 //     is taken in LDS in slot order; with more rows y[r] = W_down[e] h[r],
 //     which the library's combine sums.
 // Each touched expert's weights are read once per call, however many tokens
-// chose it (up to 16 rows at a time).
+// chose it (up to 16 rows at a time); one token, and a few that hardly share
+// experts, run each by itself.
 //
 // What bounds it is the experts' bytes.  Measured (bf16, top 8): one token of
 // 2048 x 768, gate/up 50 MB in 11.3 us and down 25 MB in 7.4 (a launch's start,

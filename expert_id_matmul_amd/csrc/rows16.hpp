@@ -40,7 +40,7 @@ constexpr uint32_t rows16_lds(int tiles) { return (uint32_t)rows16_part(tiles) *
 // return total[t][c] of lane l of wavefront v is (row 4*(l/16)+v of tile t,
 // column l%16 of tile c).  The block's four wavefronts call it together; xs
 // (rows16_lds(RT*CT) floats) may be reused after the next barrier.
-template <int DT, int RT, int CT, int D, bool NT>
+template <int DT, int RT, int CT, int D>
 __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT], const float* const (&xrow)[RT], int k,
                                                float* xs, float (&total)[RT][CT]) {
     constexpr int S = DtypeSize<DT>::value;
@@ -65,10 +65,8 @@ __device__ __forceinline__ void rows16_product(const uint8_t* const (&wrow)[CT],
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const fr_u32x4_a2* p = reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at * S + 16 * i);
-                t.w[c][i] = NT ? __builtin_nontemporal_load(p) : *p;
-            }
+            for (int i = 0; i < NP; ++i)
+                t.w[c][i] = *reinterpret_cast<const fr_u32x4_a2*>(wrow[c] + at * S + 16 * i);
 #pragma unroll
         for (int u = 0; u < RT; ++u) {
             t.x[u][0] = *reinterpret_cast<const fr_f32x4_a4*>(xrow[u] + at);
