@@ -34,7 +34,11 @@ CASES = [Lora("one_row", BF, BF, 1, 128, 256, 4, 16),
          Lora("given_odd", FL, HF, 77, 63, 45, 6, 19, given=True, pad=5),
          Lora("given_prompts", FL, BF, 2100, 264, 136, 7, 16, runs=23, given=True),
          Lora("given_f32", FL, FL, 130, 100, 70, 5, 40, runs=6, given=True),
-         Lora("long_rows", BF, BF, 5, 72, 8200, 3, 8)]
+         Lora("long_rows", BF, BF, 5, 72, 8200, 3, 8),
+         Lora("one_row_beyond_lds", BF, BF, 1, 24, 20003, 3, 8, none=0.0),
+         Lora("rows_beyond_lds", HF, FL, 7, 40, 17000, 3, 20),
+         Lora("prompts_many_ranks_f32", FL, FL, 1500, 48, 100, 3, 40, runs=5),
+         Lora("prompts_many_ranks", BF, HF, 1450, 40, 203, 4, 57, runs=8, given=True)]
 
 
 def shape_of(p):
