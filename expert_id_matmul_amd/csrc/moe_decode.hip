@@ -400,15 +400,21 @@ __global__ __launch_bounds__(64 * kWaves) void down_combine_kernel(MoeDecodeArgs
 }
 
 // ---------------------------------------------------------------- launches
-// Allows a kernel the whole LDS of a compute unit, once per device.
+// Allows a kernel as much dynamic LDS as its static LDS leaves of a compute
+// unit's (the runtime refuses more), once per device.
+constexpr uint32_t kUnitLds = 160 * 1024;
 hipError_t allow_lds(const void* kernel, std::atomic<uint64_t>& done) {
     int dev = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err != hipSuccess) return err;
     const uint64_t bit = 1ull << (dev & 63);
     if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-    err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 156 * 1024);
+    hipFuncAttributes of{};
+    err = hipFuncGetAttributes(&of, kernel);
+    if (err == hipSuccess)
+        err = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kUnitLds - of.sharedSizeBytes));
     if (err == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    else (void)hipGetLastError();  // reported here, not by the caller's next HIP call
     return err;
 }
 
