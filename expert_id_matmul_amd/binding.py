@@ -36,7 +36,8 @@ KERNELS = {1: "route", 2: "map_one_pass", 3: "map_histogram", 4: "map_scatter", 
            10: "fused_decode", 11: "silu_mul", 12: "validate", 13: "proof", 14: "split_x",
            15: "direct_split16", 16: "grouped_split16", 17: "map_split_x",
            18: "decode_gate_up", 19: "decode_down", 20: "lora_shrink", 21: "lora_expand",
-           22: "lora_base", 23: "dense_split16"}
+           22: "lora_base", 23: "dense_split16", 24: "decode_gate_up_one", 25: "decode_down_one",
+           26: "decode_down_combine"}
 DECODE_MAX_TOKENS = 64
 LORA_MAX_RANK = 256
 NO_ADAPTER = 0xFFFFFFFF

@@ -458,7 +458,7 @@ hipError_t launch_each_token(const MoeDecodeArgs& a, uint32_t cus, hipStream_t s
     const uint32_t up = block_columns(a.inter, 4, cus), down = block_columns(a.hidden, 8, cus);
     const uint32_t ub = (a.inter + up - 1) / up, db = (a.hidden + down - 1) / down;  // blocks per token
     const uint32_t up_lds = few_row_floats(a.hidden) * 4, down_lds = a.top_k * few_row_floats(a.inter) * 4;
-    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN;
+    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP_ONE, W = EIDM_KERNEL_DECODE_DOWN_ONE;
     const bool wide = a.top_k > 8;
     hipError_t err;
     if (a.n_experts <= 256)
@@ -503,7 +503,7 @@ hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream)
         return (uint32_t)(jobs < cus ? jobs : cus);
     };
     auto staged = [&](uint32_t count, uint32_t k) { return (count < row_cap(k) ? count : row_cap(k)) * few_row_floats(k) * 4; };
-    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN;
+    constexpr int U = EIDM_KERNEL_DECODE_GATE_UP, W = EIDM_KERNEL_DECODE_DOWN, WC = EIDM_KERNEL_DECODE_DOWN_COMBINE;
     constexpr uint32_t threads = 64 * kWaves;
     const bool route = a.m <= (uint32_t)kWaves && a.n_experts <= kRouteExperts;
     hipError_t err = hipSuccess;
@@ -518,8 +518,8 @@ hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream)
     if (rows <= row_cap(a.inter)) {  // every row of h fits beside the map and the output rows
         const uint32_t cols = block_columns(a.hidden, 8, cus), blocks = (a.hidden + cols - 1) / cols;
         const uint32_t lds = map_bytes + rows * 32 + staged(rows, a.inter);
-        return cols <= 4 ? launch_one<down_combine_kernel<DT, 1, 12>>(W, blocks, threads, lds, stream, a, cols)
-                         : launch_one<down_combine_kernel<DT, 2, 12>>(W, blocks, threads, lds, stream, a, cols);
+        return cols <= 4 ? launch_one<down_combine_kernel<DT, 1, 12>>(WC, blocks, threads, lds, stream, a, cols)
+                         : launch_one<down_combine_kernel<DT, 2, 12>>(WC, blocks, threads, lds, stream, a, cols);
     }
     const uint32_t blocks = blocks_of((a.hidden + 7) / 8), lds = map_bytes + staged(rows, a.inter);
     err = launch_one<down_kernel<DT, 2, 12>>(W, blocks, threads, lds, stream, a);

@@ -163,12 +163,18 @@ typedef enum eidm_kernel {
     EIDM_KERNEL_GROUPED_SPLIT16 = 16, /* split-16 Grouped                            */
     EIDM_KERNEL_MAP_SPLIT_X = 17,     /* split-16 Grouped: the one-launch map and the
                                          activation split in one launch              */
-    EIDM_KERNEL_DECODE_GATE_UP = 18,  /* few-token FFN: gate and up products, silu * up */
-    EIDM_KERNEL_DECODE_DOWN = 19,     /* few-token FFN: down product and combine      */
+    EIDM_KERNEL_DECODE_GATE_UP = 18,  /* few-token FFN: gate and up products, silu *
+                                         up of tokens that share experts' reads      */
+    EIDM_KERNEL_DECODE_DOWN = 19,     /* ... their down product (combine follows)     */
     EIDM_KERNEL_LORA_SHRINK = 20,     /* adapters: v = A x                            */
     EIDM_KERNEL_LORA_EXPAND = 21,     /* adapters: y = base + scale * B v             */
     EIDM_KERNEL_LORA_BASE = 22,       /* adapters: W x of a few rows, and their shrink */
-    EIDM_KERNEL_DENSE_SPLIT16 = 23    /* split-16 W x of many rows with one weight     */
+    EIDM_KERNEL_DENSE_SPLIT16 = 23,   /* split-16 W x of many rows with one weight     */
+    EIDM_KERNEL_DECODE_GATE_UP_ONE = 24,  /* few-token FFN, each token by itself: routing,
+                                             gate and up products, silu * up         */
+    EIDM_KERNEL_DECODE_DOWN_ONE = 25,     /* ... its down product and combine         */
+    EIDM_KERNEL_DECODE_DOWN_COMBINE = 26  /* few-token FFN: down product of tokens that
+                                             share experts' reads, and combine       */
 } eidm_kernel;
 
 /* One kernel launch: which kernel and its launch geometry (1-D grid of
