@@ -8,8 +8,8 @@
 //     is taken in LDS in slot order; with more rows y[r] = W_down[e] h[r],
 //     which the library's combine sums.
 // Each touched expert's weights are read once per call, however many tokens
-// chose it (up to 16 rows at a time); one token, and a few that hardly share
-// experts, run each by itself.
+// chose it (up to 16 rows at a time); one token, and tokens that would read
+// little again, run each by itself (each_token() below).
 //
 // What bounds it is the experts' bytes.  Measured (bf16, top 8): one token of
 // 2048 x 768, gate/up 50 MB in 11.3 us and down 25 MB in 7.4 (a launch's start,
@@ -475,27 +475,38 @@ hipError_t launch_each_token(const MoeDecodeArgs& a, uint32_t cus, hipStream_t s
                : launch_one<down_one_kernel<DT, 2, 16, 8>>(W, db * a.m, threads, down_lds, stream, a, down, db);
 }
 
-// Each token by itself when it is the only one, or when the experts that are
-// then read more than once cost less than the map and the passes of the
-// several-token form do.  That form starts some 15 us later; at some 6.5 GB/ms
-// this is 100 MB of weights, counted for evenly spread picks.  Measured at
-// 2048 x 768 bf16 (9.4 MB an expert), top 8 of 128: 2 tokens 30.6 against
-// 41.1 us, 4 tokens 55.4 against 66, 8 tokens 103 against 102; of 8 experts
-// (every token the same): 2 tokens 29.8 against 31, 3 tokens 41.5 against 32.6.
-bool each_token(const MoeDecodeArgs& a) {
+// Each token by itself when it is the only one, or when what that repeats costs
+// less than the map and the passes of the several-token form, which weigh as
+// 100 MB of weights: the shared experts' bytes, and their blocks (a turn of the
+// device's, 16 wavefronts a compute unit, as 5 MB); above kRouteExperts also
+// the routing that every block does, 40 MB a turn. There are no ids to go by:
+// picks are counted as evenly spread.
+// Over 340 layers (2-64 tokens, 4-2048 experts, 1-12 slots, rows of 16-24000,
+// spread and popular picks) the chosen form takes 4 % more than the better one
+// on average and at most twice as long (4 tokens with the same 8 of 128 experts
+// of 232 x 3856: 90 us, together 45). One by one : together, us, bf16, top 8:
+// 128 experts of 2048 x 768, 2 tokens 29 : 38 (the same picks 27 : 29), 4 tokens
+// 53 : 64 (50 : 30), 8 tokens 103 : 102; 128 of 256 x 128, 16 tokens 29 : 48, 64
+// tokens 99 : 39; 2048 of 256 x 128, 16 tokens 50 : 85, 32 tokens 94 : 66.
+bool each_token(const MoeDecodeArgs& a, uint32_t cus) {
     if (a.top_k > row_cap(a.inter)) return false;
     if (a.m == 1) return true;
     const double e = a.n_experts, rows = (double)a.m * a.top_k;
-    const double distinct = e * (1.0 - std::pow(1.0 - a.top_k / e, (double)a.m));
+    const double again = rows - e * (1.0 - std::pow(1.0 - a.top_k / e, (double)a.m));  // rows whose expert is read before
     const double expert = 3.0 * a.hidden * a.inter * (a.dtype == kDtypeF32 ? 4 : 2);
-    return (rows - distinct) * expert < 100e6;
+    const uint32_t up = block_columns(a.inter, 4, cus), down = block_columns(a.hidden, 8, cus);
+    const uint32_t ub = (a.inter + up - 1) / up, db = (a.hidden + down - 1) / down;  // wavefronts per row
+    const double turn = 16.0 * cus;
+    double cost = again * (expert + 5e6 * (ub + db) / turn);
+    if (a.n_experts > kRouteExperts) cost += 40e6 * rows * ub / turn;
+    return cost < 100e6;
 }
 
 template <int DT>
 hipError_t launch_dt(const MoeDecodeArgs& a, int device_cus, hipStream_t stream) {
     const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
     const uint32_t rows = a.m * a.top_k;
-    if (each_token(a)) return launch_each_token<DT>(a, cus, stream);
+    if (each_token(a, cus)) return launch_each_token<DT>(a, cus, stream);
     const uint32_t touched = few_map_ids(rows, a.n_experts);  // at most
     const uint32_t map_bytes = few_map_words(rows, a.n_experts) * 4;
     auto blocks_of = [&](uint32_t groups) {

@@ -426,11 +426,13 @@ int eidm_moe_ffn(const eidm_ffn_shape* shape, int route, const void* w_gate, con
  * The expert FFN of a few tokens (a decode step of up to
  * EIDM_DECODE_MAX_TOKENS requests): the computation, the arguments and the
  * bits of eidm_moe_ffn, reading each touched expert's three matrices once
- * for up to 16 of the rows that chose it.  A token by itself, and a few that
- * share hardly any expert, take two launches (routing, gate, up and
- * silu * up; down and combine); other calls share the experts' reads between
- * tokens, with a launch of their own for routing (m > 8 or n_experts > 256)
- * and for combine (rows of h beyond a block's LDS).  Every form has the same
+ * for up to 16 of the rows that chose it.  A token by itself takes two
+ * launches (routing, gate, up and silu * up; down and combine), and so do
+ * tokens that, were their picks spread evenly, would read so little again that
+ * sharing costs more: there an expert's matrices are read once per row.  Other
+ * calls share the experts' reads between tokens, with a launch of their own
+ * for routing (m > 8 or n_experts > 256) and for combine (rows of h beyond a
+ * block's LDS).  Every form has the same
  * bits, and a token's results depend on no other token.
  * Requires m <= EIDM_DECODE_MAX_TOKENS, top_k <= 16, hidden and inter <=
  * 32768 and the router's limits (else EIDM_E_UNSUPPORTED).  Weights need the
