@@ -218,13 +218,22 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
 
 }  // namespace
 
-// Half the compute units have a tile.  Against eidm_matmul_id's kernels for
-// the same product (bf16, us, this : those): 128 tiles, k 4096 118 : 111,
-// k 512 30 : 35; 192 tiles, k 4096 124 : 158; 512 tiles, k 4096 210 : 401.
-// Below it those are the faster ones (96 tiles of k 4096 take them 87, and
-// one tile on one compute unit takes this kernel 100).
-bool dense_split16_supported(uint32_t m, uint32_t n, int device_cus) {
-    return (uint64_t)((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile) * 4 >= (uint64_t)device_cus * 2;
+// The tiles fill half the device; nine sixteenths of it with k above 2048, all
+// of it where the tiles themselves are far from full (up to 64 rows) or each
+// split row serves few columns. Up to 32 rows are one row tile of
+// eidm_matmul_id's kernels, which then read the weights once as well.
+// Over 330 products (m 1 - 32768, n 64 - 131072, k 128 - 4096) the chosen one
+// takes 0.6 % more than the better one on average, 16 % at most. Whole calls,
+// bf16, us, this : those: 1 x 16384 x 4096 121 : 46, 64 x 16384 x 4096 133 : 77,
+// 96 x 16384 x 4096 140 : 117, 32 x 65536 x 512 49 : 45, 64 x 65536 x 512 58 : 69,
+// 1024 x 2048 x 4096 135 : 126, 1024 x 2048 x 1024 56 : 59, 1500 x 1500 x 4096
+// 147 : 175, 1024 x 4096 x 4096 140 : 222, 12000 x 200 x 4096 351 : 309.
+bool dense_split16_supported(uint32_t m, uint32_t n, uint32_t k, int device_cus) {
+    const uint64_t cus = device_cus > 0 ? (uint64_t)device_cus : 256;
+    if (m <= 32) return false;
+    const uint64_t tiles = (uint64_t)((m + kTile - 1) / kTile) * ((n + kTile - 1) / kTile);
+    const bool whole = m <= 64 || (uint64_t)n * 8 <= k;
+    return tiles * 16 >= cus * (whole ? 16 : k > 2048 ? 9 : 8);
 }
 
 uint64_t dense_split16_bytes(uint32_t m, uint32_t k) {

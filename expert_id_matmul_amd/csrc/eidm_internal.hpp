@@ -107,7 +107,7 @@ hipError_t launch_direct_split16(const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_grouped_split16(const MatmulArgs& a, const MapBuffers& buf, int device_cus, hipStream_t stream);
 // one expert's product of many rows in the split-16 arithmetic (a.xsplit:
 // dense_split16_bytes(m, k) of scratch; a.ids is not read)
-bool dense_split16_supported(uint32_t m, uint32_t n, int device_cus);
+bool dense_split16_supported(uint32_t m, uint32_t n, uint32_t k, int device_cus);
 uint64_t dense_split16_bytes(uint32_t m, uint32_t k);
 hipError_t launch_dense_split16(const MatmulArgs& a, int device_cus, hipStream_t stream);
 hipError_t launch_combine(uint32_t m, uint32_t top_k, uint32_t n, const float* y,

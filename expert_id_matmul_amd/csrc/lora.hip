@@ -652,7 +652,7 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
     if (weights && shape->arith == EIDM_ARITH_F32 && eidm::lora_base_few_supported(a, cus)) {
         err = eidm::launch_lora_base_few(a, shape->weight_dtype, static_cast<const uint8_t*>(weights), cus, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "projection launch: %s", hipGetErrorString(err));
-    } else if (weights && shape->arith == EIDM_ARITH_SPLIT16 && eidm::dense_split16_supported(a.m, a.n, cus)) {
+    } else if (weights && shape->arith == EIDM_ARITH_SPLIT16 && eidm::dense_split16_supported(a.m, a.n, a.k, cus)) {
         err = eidm::launch_lora_shrink(a, cus, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "adapter shrink launch: %s", hipGetErrorString(err));
         eidm::MatmulArgs p{};
