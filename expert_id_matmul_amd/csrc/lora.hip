@@ -3,8 +3,8 @@
 //     reduction order), a = the row's adapter;
 //   expand: out[t] = base[t] + scale_a * (B_a v[t]).
 // The shared projection beside them (base = W x), when the call computes it:
-//   * up to 3 tiles of 32 x 32 outputs a compute unit: base_few_kernel here,
-//     the F32 order;
+//   * up to four rows, and up to 3 tiles of 32 x 32 outputs a compute unit:
+//     base_few_kernel here, the F32 order;
 //   * many rows in the split-16 arithmetic: dense_split16.hip;
 //   * else eidm_matmul_id with one expert.  The same bits in each.
 //
@@ -344,6 +344,9 @@ constexpr uint32_t kRowLds = 64 * 1024;  // LDS of staged rows
 
 bool stages_rows(uint32_t rows, uint32_t k) { return (uint64_t)rows * few_row_floats(k) * 4 <= kRowLds; }
 
+// the projection's form that stages all rows (base_few_kernel, CT = 0)
+bool few_rows_staged(const LoraArgs& a) { return a.m <= 4 && stages_rows(a.m, a.k); }
+
 template <int DT>
 hipError_t shrink_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
     const uint32_t parts = (a.max_rank + 15) / 16;
@@ -401,7 +404,7 @@ uint64_t makespan(const LoraArgs& a, uint32_t rt, uint32_t ct, uint32_t each, ui
 template <int DT>
 hipError_t base_few_dt(const LoraArgs& a, const uint8_t* weights, bool with_shrink, int device_cus, hipStream_t stream) {
     const uint32_t cus = device_cus > 0 ? (uint32_t)device_cus : 256;
-    if (a.m <= 4 && stages_rows(a.m, a.k))
+    if (few_rows_staged(a))
         return a.m == 1 ? base_few<DT, 0, 0>(a, weights, with_shrink, cus, stream)
                         : base_few<DT, 1, 0>(a, weights, with_shrink, cus, stream);
     // larger tiles read less per product, smaller ones spread more evenly; one
@@ -444,9 +447,13 @@ hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t str
     }
 }
 
-// The library's Grouped kernels take over where the 32x32 tiles fill the
-// device more than three times (they share activations through LDS).
+// Up to four rows staged in LDS: at any n (k 4096, bf16, us, this : the
+// library's Direct or Grouped kernels: 1 x 32768 45 : 53, 2 x 32768 48 : 77,
+// 4 x 65536 125 : 133; k 512, 4 x 65536 31 : 34). More rows: the Grouped kernels
+// take over where the 32x32 tiles fill the device more than three times (they
+// share activations through LDS).
 bool lora_base_few_supported(const LoraArgs& a, int device_cus) {
+    if (few_rows_staged(a) && (a.n + 15) / 16 < (1u << 23)) return true;  // (a grid of below 2^32 threads)
     return ((uint64_t)a.m + 31) / 32 * ((a.n + 31) / 32) <= (uint64_t)device_cus * 3;
 }
 

@@ -48,3 +48,12 @@ def test_dense_split16_tiles_only_where_they_are_the_faster_ones(lib, m, n, k, d
     of a narrow one, take eidm_matmul_id's kernels (measured at these sizes)."""
     print(f"[case] {m} {n} {k}", flush=True)
     assert ("dense_split16" in projection(lib, BF, m, n, k, B.ARITH_SPLIT16)) == dense
+
+
+@pytest.mark.parametrize("dtype,m,n,k", [(BF, 1, 24592, 520), (HF, 1, 40007, 260), (FL, 1, 33000, 200), (BF, 2, 32768, 1024),
+                                         (BF, 4, 65536, 512), (HF, 3, 50001, 129), (FL, 4, 30011, 140)])
+def test_up_to_four_rows_are_staged_at_any_width(lib, dtype, m, n, k):
+    """A vocabulary's width for a few rows: one launch with the adapters'
+    shrink, then the expand."""
+    print(f"[case] {dtype} {m} {n} {k}", flush=True)
+    assert projection(lib, dtype, m, n, k, B.ARITH_F32) == ["lora_base", "lora_expand"]
