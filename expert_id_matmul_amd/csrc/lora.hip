@@ -38,6 +38,8 @@
 namespace eidm {
 namespace {
 
+constexpr uint32_t kXcds = 8;
+
 __device__ __forceinline__ uint32_t rank_of(const LoraArgs& a, uint32_t id) {
     return a.ranks ? min(a.ranks[id], a.max_rank) : a.max_rank;
 }
@@ -127,12 +129,13 @@ __global__ __launch_bounds__(256) void base_few_kernel(LoraArgs a, const uint8_t
                                      if (col < a.n) a.out[(size_t)t * a.n + col] = v[0];
                                  });
     } else {
-        // block (column tile, row tile), the row tiles of one column tile on
-        // one XCD, whose L2 then serves the weights to all but the first
+        // each XCD (blocks are dealt to them in turn) takes an equal share of
+        // the tiles, the row tiles of a column tile one after the other, so
+        // that its L2 serves the weights to all but the first
         const uint32_t rtiles = (a.m + 16 * RT - 1) / (16 * RT), i = lane & 15;
-        const uint32_t group = block / (8 * rtiles), in = block % (8 * rtiles);
-        const uint32_t col0 = (group * 8 + in % 8) * 16 * CT, row0 = in / 8 * 16 * RT;
-        if (col0 >= a.n) return;  // the last group of column tiles
+        const uint32_t tile = block % kXcds * (bases / kXcds) + block / kXcds;
+        const uint32_t col0 = tile / rtiles * 16 * CT, row0 = tile % rtiles * 16 * RT;
+        if (col0 >= a.n) return;  // past the last tile
         const uint8_t* wrow[CT];
         const float* xrow[RT];
 #pragma unroll
@@ -385,7 +388,7 @@ template <int DT, int RT, int CT>
 hipError_t base_few(const LoraArgs& a, const uint8_t* weights, bool with_shrink, uint32_t cus, hipStream_t stream) {
     constexpr uint32_t C = CT ? 16 * CT : 16, R = CT ? 16 * RT : 1;
     const uint32_t ctiles = (a.n + C - 1) / C, rtiles = (a.m + R - 1) / R;
-    const uint32_t blocks = CT ? (ctiles + 7) / 8 * 8 * rtiles : ctiles;
+    const uint32_t blocks = CT ? (ctiles * rtiles + kXcds - 1) / kXcds * kXcds : ctiles;
     const uint32_t parts = shrink_parts(a, ctiles * rtiles, cus), shrinks = with_shrink ? a.m * parts : 0;
     uint32_t lds = CT ? rows16_lds(RT * CT) * 4 : a.m * few_row_floats(a.k) * 4;
     if (with_shrink && lds < few_row_floats(a.k) * 4) lds = few_row_floats(a.k) * 4;
