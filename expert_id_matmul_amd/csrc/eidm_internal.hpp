@@ -143,7 +143,7 @@ struct LoraArgs {
     float *v, *out;
     uint32_t* zero_ids;  // [m] ids of the shared projection, written by the shrink (or null)
     // the id -> row map of the rows (null: the row forms)
-    const uint32_t *counts, *offsets, *rows;
+    const uint32_t *offsets, *rows;
     uint32_t* tiles;  // the sorted rows in tiles of 16, written by the shrink
 };
 // rows up to which each reads its adapter by itself at any rank; more are

@@ -550,8 +550,10 @@ int lora_sizes(const eidm_lora_shape* f, bool shared, LoraSizes* z) {
     z->off_hist = align256((uint64_t)f->m * z->v_stride * 4);
     z->off_counts = z->off_offsets = z->off_rows = z->off_tiles = z->off_ids = z->off_hist;
     if (lora_sorts_rows(f->m, f->k, f->max_rank)) {
-        const uint64_t parts = ((uint64_t)f->n + 255) / 256;  // a launch has a block per slot and part
-        if (lora_slots(f->m, f->n_adapters) * parts > 0x7fffffffull)
+        // a launch has a block of 256 threads per slot and 256 columns or 32
+        // ranks, and fewer than 2^32 threads
+        const uint64_t columns = ((uint64_t)f->n + 255) / 256, ranks = (f->max_rank + 31) / 32;
+        if (lora_slots(f->m, f->n_adapters) * std::max(columns, ranks) >= 1u << 24)
             return api_fail(EIDM_E_UNSUPPORTED, "the adapters' grid for %u rows of %u columns is too large", f->m, f->n);
         z->off_counts = z->off_hist + align256(map_hist_elements(f->m, f->n_adapters) * 4);
         z->off_offsets = z->off_counts + align256((uint64_t)(f->n_adapters + 1) * 4);
@@ -562,6 +564,8 @@ int lora_sizes(const eidm_lora_shape* f, bool shared, LoraSizes* z) {
     z->off_matmul = z->off_ids + align256((uint64_t)f->m * 4);
     z->weights = z->matmul = 0;
     if (shared) {
+        if (f->m == 1 && f->n >= 1u << 29)  // the Direct route's 128 threads per 16 columns
+            return api_fail(EIDM_E_UNSUPPORTED, "the projection's grid for one row of %u columns is too large", f->n);
         const eidm_shape s = shared_projection(f);
         eidm_requirements q{};
         q.struct_size = sizeof(q);
@@ -654,7 +658,6 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
         const eidm::MapBuffers buf{at(z.off_hist), at(z.off_counts), at(z.off_offsets), at(z.off_rows)};
         err = eidm::launch_map(adapter_ids, a.m, a.n_adapters, buf, st);
         if (err != hipSuccess) return api_fail(EIDM_E_DEVICE, "map launch: %s", hipGetErrorString(err));
-        a.counts = buf.counts;
         a.offsets = buf.offsets;
         a.rows = buf.rows;
         a.tiles = at(z.off_tiles);

@@ -489,8 +489,11 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
  *               and mean nothing afterwards, and calls that may overlap in
  *               time need one each
  * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m, n and k as
- * for eidm_matmul_id, and a launch's grid: (m / 16 + n_adapters + 1) *
- * ceil(n / 256) < 2^31 (else EIDM_E_UNSUPPORTED).
+ * for eidm_matmul_id, and fewer than 2^32 threads a launch (else
+ * EIDM_E_UNSUPPORTED): where rows are sorted by adapter (above 64 rows with
+ * m * max_rank > 12288, and with k above 16256) (m / 16 + n_adapters + 1) *
+ * max(ceil(n / 256), ceil(max_rank / 32)) < 2^24; with weights and one row
+ * n < 2^29.
  */
 typedef struct eidm_lora_shape {
     uint32_t struct_size;    /* sizeof(eidm_lora_shape) */

@@ -173,3 +173,22 @@ def test_lora_split16_keeps_that_arithmetics_conditions(lib):
     s = lora(arith=B.ARITH_SPLIT16)
     assert linear(lib, s, x=FAKE + 4) == B.E_ALIGN
     assert linear(lib, s, w=FAKE + 8) == B.E_ALIGN
+
+
+# HIP takes fewer than 2^32 threads a launch: 2^24 blocks of 256
+@pytest.mark.parametrize("m,n,k,adapters,max_rank,code", [
+    (1 << 25, 64, 64, 4, 256, B.E_UNSUPPORTED),          # the shrink's blocks: 32 ranks each
+    ((1 << 25) - 16 * 6, 64, 64, 4, 256, 0),
+    (1, 8188 * 256 + 1, 16385, 2048, 1, B.E_UNSUPPORTED),  # the expand's: 256 columns each, many adapters
+    (1, 8188 * 256, 16385, 2048, 1, 0),
+    (1, 1 << 29, 8, 2, 4, B.E_UNSUPPORTED),              # the projection of one row
+    (1, (1 << 29) - 16, 8, 2, 4, 0)])
+def test_lora_grids_stay_below_a_launchs_threads(lib, m, n, k, adapters, max_rank, code):
+    s = B.make_lora_shape(B.BF16, B.BF16, m, n, k, adapters, max_rank)
+    assert linear(lib, s, abytes=1 << 50, bbytes=1 << 50, wbytes=1 << 50, sbytes=0) == (code or B.E_SIZE)
+    assert (lib.lib.eidm_lora_linear_scratch_bytes(ctypes.byref(s)) == 0) == (code != 0)
+
+
+def test_lora_one_row_on_a_base_has_no_projection_to_refuse(lib):
+    s = B.make_lora_shape(B.BF16, B.BF16, 1, 1 << 29, 8, 2, 4)
+    assert linear(lib, s, w=None, base=FAKE, abytes=1 << 50, bbytes=1 << 50, sbytes=0) == B.E_SIZE
