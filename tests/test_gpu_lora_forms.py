@@ -1,12 +1,15 @@
 """Which kernels eidm_lora_linear takes, by the dispatch receipt, and their
 bits: the shared projection's forms against eidm_matmul_id's Direct route, the
 adapters' forms against the documented order."""
+import numpy as np
 import pytest
 import torch
 
 from expert_id_matmul_amd import binding as B
 from expert_id_matmul_amd import workloads as W
 from helpers import check_guarded, poisoned_output
+from lora_cases import Lora, base_bits, documented, inputs
+from test_gpu_lora import Call, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +72,105 @@ def test_projection_tiles_are_spread_over_all_xcds(lib, dtype, m, n, k):
     assert receipt.kernels()[-3:] == ["lora_shrink", "lora_base", "lora_expand"]
     tiles = {(-(-m // (16 * r))) * (-(-n // (16 * c))) for r, c in ((1, 1), (1, 2), (2, 2), (2, 3))}
     assert receipt.launches[receipt.recorded - 2].grid in {-(-t // 8) * 8 for t in tiles}
+
+
+@pytest.mark.parametrize("dtype,m,n,k,a_dtype", [(BF, 900, 1003, 137, None), (HF, 1031, 2000, 264, FL), (FL, 512, 2048, 300, None),
+                                                 (BF, 512, 4096, 1024, None), (BF, 5, 131072, 64, None)])
+def test_projections_beyond_the_small_tiles(lib, dtype, m, n, k, a_dtype):
+    """More than three 32 x 32 tiles a compute unit, the ordinary prompt chunk:
+    the F32 order through eidm_matmul_id, its ids written by the shrink."""
+    print(f"[case] {dtype} {m} {n} {k}", flush=True)
+    kernels = projection(lib, dtype, m, n, k, B.ARITH_F32, a_dtype).kernels()
+    assert kernels[0] == "lora_shrink" and kernels[-1] == "lora_expand" and "lora_base" not in kernels
+    assert kernels[-2].startswith("grouped")
+
+
+SORTED = ["lora_shrink", "lora_expand"]  # behind a map
+
+
+@pytest.mark.parametrize("p", [Lora("chunk", BF, BF, 800, 1024, 264, 6, 16, runs=4),
+                               Lora("chunk_odd", HF, FL, 1201, 1003, 139, 9, 11, runs=7, pad=3),
+                               Lora("adapters_65", BF, BF, 900, 96, 128, 65, 16),
+                               Lora("adapters_130", BF, HF, 1000, 77, 131, 130, 20, pad=1),
+                               Lora("adapters_300_given", FL, BF, 777, 130, 96, 300, 24, given=True),
+                               Lora("most_adapters", BF, BF, 100, 40, 96, 2048, 200),
+                               Lora("most_adapters_f32", FL, FL, 4000, 33, 64, 2048, 9, given=True),
+                               Lora("one_adapter_of_many", BF, BF, 400, 64, 96, 500, 64, runs=1, none=0.0),
+                               Lora("two_of_many", HF, HF, 333, 70, 88, 200, 48, runs=3, given=True)],
+                         ids=lambda p: p.name)
+def test_rows_sorted_over_many_adapters(lib, p):
+    print(f"[case] {p.name}", flush=True)
+    d = inputs(p)
+    call = Call(lib, p, d)
+    got = call.result(nan=True)
+    kernels = lib.last_dispatch().kernels()
+    assert kernels[0].startswith("map") and set(SORTED) <= set(kernels)
+    same_bits(got, documented(p, d, base_bits(p, d)))
+
+
+def test_sorted_rows_at_the_adapters_ends(lib):
+    """First and last adapter, adapters whose rows end at, before and behind a
+    tile's 16, ids without an adapter and bad ids beside them."""
+    p = Lora("ends", BF, BF, 1024, 48, 72, 150, 16, given=True, none=0.0)
+    d = inputs(p)
+    ids = d["ids"]
+    ids[:] = 149
+    at = 0
+    for a, rows in ((0, 16), (63, 15), (64, 17), (65, 1), (127, 32), (128, 33), (0xFFFFFFFF, 31), (150, 2), (0x7FFFFFFF, 1)):
+        ids[at: at + rows] = a
+        at += rows
+    ids[:] = np.random.default_rng(3).permutation(ids)
+    call = Call(lib, p, d)
+    got = call.result(nan=True)
+    assert lib.last_dispatch().kernels()[0].startswith("map")
+    same_bits(got, documented(p, d, base_bits(p, d)))
+
+
+@pytest.mark.parametrize("p", [Lora("staged_to_the_end", BF, BF, 3, 40, 16256, 4, 8, none=0.0),
+                               Lora("staged_four", HF, HF, 4, 40, 3984, 4, 8, none=0.0),
+                               Lora("staged_one", FL, FL, 1, 40, 16256, 4, 8, none=0.0),
+                               Lora("beyond", BF, BF, 3, 40, 16257, 4, 8, none=0.0),
+                               Lora("given_one", FL, BF, 1, 300, 520, 6, 16, given=True, none=0.0),
+                               Lora("given_few", FL, HF, 33, 131, 77, 6, 12, given=True)], ids=lambda p: p.name)
+def test_rows_at_the_staging_limit(lib, p):
+    print(f"[case] {p.name}", flush=True)
+    d = inputs(p)
+    call = Call(lib, p, d)
+    got = call.result()
+    assert lib.last_dispatch().kernels()[0].startswith("map") == (p.k > 16256)
+    same_bits(got, documented(p, d, base_bits(p, d)))
+
+
+@pytest.mark.parametrize("ps", [(Lora("many", BF, BF, 900, 256, 136, 130, 16), Lora("chunk", BF, BF, 800, 1024, 264, 6, 16, runs=4)),
+                                (Lora("wide", BF, BF, 2, 32768, 136, 8, 16), Lora("few", BF, FL, 9, 256, 136, 8, 16))],
+                         ids=["sorted", "rows"])
+def test_two_graphs_that_share_a_scratch(lib, ps):
+    """Replayed in turn on new rows and adapters, with eager work between."""
+    calls = [Call(lib, p, inputs(p)) for p in ps]
+    scratch = max((c.scratch for c in calls), key=lambda t: t.numel())
+    graphs = []
+    for call in calls:
+        call.scratch = scratch
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    g = torch.Generator().manual_seed(6)
+    for rep in range(5):
+        want = []
+        for call in calls:
+            p = call.p
+            call.x.copy_(torch.randn(p.m, p.k, generator=g))
+            call.ids.copy_(torch.randint(-1, p.n_adapters, (p.m,), generator=g).int())
+            call()
+            torch.cuda.synchronize()
+            want.append(call.out.clone())
+            call.out[: p.m * p.n].zero_()
+        scratch.fill_(rep * 41)
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for call, w in zip(calls, want):
+            assert torch.equal(call.out.view(torch.int32), w.view(torch.int32)), rep
