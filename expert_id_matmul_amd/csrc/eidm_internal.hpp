@@ -146,10 +146,10 @@ struct LoraArgs {
     const uint32_t *offsets, *rows;
     uint32_t* tiles;  // the sorted rows in tiles of 16, written by the shrink
 };
-// rows up to which each reads its adapter by itself at any rank; more are
-// sorted by adapter when rows times ranks make that the faster form
+// rows up to which each reads its adapter by itself (a row that a block can
+// stage); more are sorted by adapter when that is the faster form
 constexpr uint32_t kLoraRowForm = 64;
-bool lora_sorts_rows(uint32_t m, uint32_t k, uint32_t max_rank);
+bool lora_sorts_rows(uint32_t m, uint32_t n, uint32_t k, uint32_t n_adapters, uint32_t max_rank);
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream);
 // out = W x for up to some hundred rows (any alignment), and the shrink of them
 bool lora_base_few_supported(const LoraArgs& a, int device_cus);

@@ -435,10 +435,19 @@ hipError_t expand_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
 
 }  // namespace
 
-bool lora_sorts_rows(uint32_t m, uint32_t k, uint32_t max_rank) {
-    // measured on k = 768 .. 4096: rank 16 crosses between 500 and 1000 rows,
-    // rank 64 at 200
-    return (m > kLoraRowForm && (uint64_t)m * max_rank > 12288) || !stages_rows(1, k);
+// By rows, every row reads its own adapter; sorted, there are a map and a slot
+// per adapter, whether it has rows or not, in both launches. Over 1560 calls
+// (m 64 - 4000, n + k 640 - 8192, rank 4 - 256, 4 - 2048 adapters, with a
+// projection beside them and on given rows, scattered ids and runs) the chosen
+// form takes 1.2 % more than the better one on average. Given rows, bf16, us,
+// by rows : sorted: 200 x 128 x 512, rank 64, 32 adapters 12 : 18, 256 adapters
+// 12 : 22, 2048 adapters 13 : 77; 400 x 3000 x 200, rank 64, 256 adapters 55 : 28;
+// 1600 x 4096 x 4096, rank 4, 32 adapters 58 : 31; rank 64, 2048 adapters 262 : 135.
+bool lora_sorts_rows(uint32_t m, uint32_t n, uint32_t k, uint32_t n_adapters, uint32_t max_rank) {
+    if (!stages_rows(1, k)) return true;  // the row form stages a row
+    const double read = (double)m * (max_rank + 4) * ((double)n + k);
+    const double slots = (double)n_adapters * ((max_rank + 31) / 32 + (n + 255) / 256);  // blocks of empty slots
+    return m > kLoraRowForm && read > 30e6 + 16e3 * slots;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream) {
@@ -549,7 +558,7 @@ int lora_sizes(const eidm_lora_shape* f, bool shared, LoraSizes* z) {
     z->v_stride = (f->max_rank + 7) / 8 * 8;
     z->off_hist = align256((uint64_t)f->m * z->v_stride * 4);
     z->off_counts = z->off_offsets = z->off_rows = z->off_tiles = z->off_ids = z->off_hist;
-    if (lora_sorts_rows(f->m, f->k, f->max_rank)) {
+    if (lora_sorts_rows(f->m, f->n, f->k, f->n_adapters, f->max_rank)) {
         // a launch has a block of 256 threads per slot and 256 columns or 32
         // ranks, and fewer than 2^32 threads
         const uint64_t columns = ((uint64_t)f->n + 255) / 256, ranks = (f->max_rank + 31) / 32;
@@ -653,7 +662,7 @@ int eidm_lora_linear(const eidm_lora_shape* shape, const void* weights, uint64_t
     a.out = output;
     const int cus = eidm::device_cus();
     hipError_t err;
-    if (eidm::lora_sorts_rows(a.m, a.k, a.max_rank)) {
+    if (eidm::lora_sorts_rows(a.m, a.n, a.k, a.n_adapters, a.max_rank)) {
         auto at = [&](uint64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
         const eidm::MapBuffers buf{at(z.off_hist), at(z.off_counts), at(z.off_offsets), at(z.off_rows)};
         err = eidm::launch_map(adapter_ids, a.m, a.n_adapters, buf, st);

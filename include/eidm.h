@@ -490,8 +490,8 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
  *               time need one each
  * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m, n and k as
  * for eidm_matmul_id, and fewer than 2^32 threads a launch (else
- * EIDM_E_UNSUPPORTED): where rows are sorted by adapter (above 64 rows with
- * m * max_rank > 12288, and with k above 16256) (m / 16 + n_adapters + 1) *
+ * EIDM_E_UNSUPPORTED): where rows are sorted by adapter (with k above 16256,
+ * and where that is faster, above 64 rows) (m / 16 + n_adapters + 1) *
  * max(ceil(n / 256), ceil(max_rank / 32)) < 2^24; with weights and one row
  * n < 2^29.
  */

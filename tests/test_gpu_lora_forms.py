@@ -88,15 +88,20 @@ def test_projections_beyond_the_small_tiles(lib, dtype, m, n, k, a_dtype):
 SORTED = ["lora_shrink", "lora_expand"]  # behind a map
 
 
-@pytest.mark.parametrize("p", [Lora("chunk", BF, BF, 800, 1024, 264, 6, 16, runs=4),
-                               Lora("chunk_odd", HF, FL, 1201, 1003, 139, 9, 11, runs=7, pad=3),
-                               Lora("adapters_65", BF, BF, 900, 96, 128, 65, 16),
-                               Lora("adapters_130", BF, HF, 1000, 77, 131, 130, 20, pad=1),
-                               Lora("adapters_300_given", FL, BF, 777, 130, 96, 300, 24, given=True),
-                               Lora("most_adapters", BF, BF, 100, 40, 96, 2048, 200),
-                               Lora("most_adapters_f32", FL, FL, 4000, 33, 64, 2048, 9, given=True),
-                               Lora("one_adapter_of_many", BF, BF, 400, 64, 96, 500, 64, runs=1, none=0.0),
-                               Lora("two_of_many", HF, HF, 333, 70, 88, 200, 48, runs=3, given=True)],
+@pytest.mark.parametrize("p", [Lora("chunk", BF, BF, 1300, 1024, 264, 6, 16, runs=4),
+                               Lora("chunk_odd", HF, FL, 1900, 1003, 139, 9, 11, runs=7, pad=3),
+                               Lora("chunk_f32", FL, FL, 1290, 611, 300, 4, 33, runs=5),
+                               Lora("adapters_65", BF, BF, 1400, 700, 628, 65, 16),
+                               Lora("adapters_130", BF, HF, 1200, 577, 431, 130, 33, pad=1),
+                               Lora("adapters_300_given", FL, BF, 1200, 830, 996, 300, 24, given=True),
+                               Lora("most_adapters", BF, BF, 2700, 250, 900, 2048, 40),
+                               Lora("most_adapters_f32", FL, FL, 9500, 233, 600, 2048, 9, given=True),
+                               Lora("one_adapter_of_many", BF, BF, 1300, 300, 500, 500, 64, runs=1, none=0.0),
+                               Lora("two_of_many", HF, HF, 1000, 270, 588, 200, 48, runs=3, given=True),
+                               Lora("long_k_f32", FL, FL, 37, 63, 16300, 6, 19),
+                               Lora("long_k_odd", HF, BF, 70, 77, 16301, 5, 41, pad=1),
+                               Lora("long_k_most_ranks", BF, BF, 50, 130, 16264, 3, 256, given=True, ranks=False),
+                               Lora("long_k_many_adapters", FL, HF, 65, 1, 16259, 300, 40, given=True, pad=3)],
                          ids=lambda p: p.name)
 def test_rows_sorted_over_many_adapters(lib, p):
     print(f"[case] {p.name}", flush=True)
@@ -108,10 +113,29 @@ def test_rows_sorted_over_many_adapters(lib, p):
     same_bits(got, documented(p, d, base_bits(p, d)))
 
 
+@pytest.mark.parametrize("m,n,k,adapters,rank,sorts", [
+    (200, 128, 512, 2048, 64, False), (200, 128, 512, 256, 64, False), (800, 128, 512, 2048, 16, False),
+    (100, 1024, 1024, 2048, 256, False), (400, 3000, 200, 256, 64, False), (400, 3000, 200, 32, 64, True),
+    (1600, 4096, 4096, 32, 4, True), (1600, 4096, 4096, 256, 64, True)])
+def test_rows_are_sorted_only_where_that_is_faster(lib, m, n, k, adapters, rank, sorts):
+    """A slot per adapter costs more than it saves a few rows of many adapters
+    (up to seven times the time); many rows and long ones gain up to half."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    rnd = lambda *z: torch.randn(*z, generator=g, device="cuda")
+    x, base = rnd(m, k), rnd(m, n)
+    a, b = (rnd(adapters, rank, k) * k ** -0.5).bfloat16(), rnd(adapters, n, rank).bfloat16()
+    ids = torch.randint(0, adapters, (m,), generator=g, device="cuda").int()
+    shape = B.make_lora_shape(BF, BF, m, n, k, adapters, rank)
+    scratch = torch.empty(lib.lora_linear_scratch_bytes(shape), dtype=torch.uint8, device="cuda")
+    out = torch.empty(m, n, device="cuda")
+    lib.lora_linear(shape, None, base, a, b, None, None, x, ids, out, scratch)
+    assert lib.last_dispatch().kernels()[0].startswith("map") == sorts
+
+
 def test_sorted_rows_at_the_adapters_ends(lib):
     """First and last adapter, adapters whose rows end at, before and behind a
     tile's 16, ids without an adapter and bad ids beside them."""
-    p = Lora("ends", BF, BF, 1024, 48, 72, 150, 16, given=True, none=0.0)
+    p = Lora("ends", BF, BF, 1300, 480, 1000, 150, 16, given=True, none=0.0)
     d = inputs(p)
     ids = d["ids"]
     ids[:] = 149
@@ -141,7 +165,7 @@ def test_rows_at_the_staging_limit(lib, p):
     same_bits(got, documented(p, d, base_bits(p, d)))
 
 
-@pytest.mark.parametrize("ps", [(Lora("many", BF, BF, 900, 256, 136, 130, 16), Lora("chunk", BF, BF, 800, 1024, 264, 6, 16, runs=4)),
+@pytest.mark.parametrize("ps", [(Lora("many", BF, BF, 1500, 700, 628, 130, 16), Lora("chunk", BF, BF, 1300, 1024, 264, 6, 16, runs=4)),
                                 (Lora("wide", BF, BF, 2, 32768, 136, 8, 16), Lora("few", BF, FL, 9, 256, 136, 8, 16))],
                          ids=["sorted", "rows"])
 def test_two_graphs_that_share_a_scratch(lib, ps):
