@@ -29,13 +29,10 @@
 // theorem statement (one order, whichever rows are computed together).
 #include "eidm_device.hpp"
 #include "eidm_internal.hpp"
+#include "split16.hpp"
 
 namespace eidm {
 namespace {
-
-typedef unsigned int ds_u32x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 ds_f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 ds_bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 128;           // rows and columns of a block
 constexpr int kWaveRows = 2;         // 16-row tiles per wavefront
@@ -44,31 +41,9 @@ constexpr uint32_t kAhead = 2;       // steps of activations in registers
 constexpr uint32_t kXcds = 8, kGroup = 64;  // XCDs; tiles of one XCD side by side
 constexpr uint32_t kPartBytes = 1024;        // one part of 16 rows and 32 k: lane l's row l%16, chunk l/16
 
-template <int DT>
-__device__ __forceinline__ f32x4 product(const ds_u32x4& a, const ds_u32x4& b, f32x4 c) {
-    if constexpr (DT == kDtypeF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(ds_f16x8, a), __builtin_bit_cast(ds_f16x8, b), c,
-                                                      0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(ds_bf16x8, a),
-                                                       __builtin_bit_cast(ds_bf16x8, b), c, 0, 0, 0);
-}
-
-// f32 -> 16-bit, round to nearest even (infinities and NaN kept), and back
-template <int DT> __device__ __forceinline__ uint32_t to16(float v) {
-    if constexpr (DT == kDtypeF16) {
-        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
-    } else {
-        const uint32_t u = __float_as_uint(v);
-        if ((u & 0x7f800000u) == 0x7f800000u) return (u >> 16) | ((u & 0xffffu) ? 0x40u : 0u);
-        return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    }
-}
-
 __host__ __device__ inline uint32_t split_steps(uint32_t k) { return (k + 127) / 128 * 4; }  // of 32, zeros past k
 
-// x = p1 + p2 + p3 (each rounded from what is left; a non-finite x keeps p1
-// alone), one thread per (row, 8 elements).
+// The three parts of x (split16.hpp), one thread per (row, 8 elements).
 template <int DT>
 __global__ __launch_bounds__(256) void pack_split16_kernel(const float* __restrict__ x, uint32_t m, uint32_t k,
                                                            uint8_t* __restrict__ packed) {
@@ -82,22 +57,14 @@ __global__ __launch_bounds__(256) void pack_split16_kernel(const float* __restri
             const f32x4* src = reinterpret_cast<const f32x4*>(x + (size_t)row * k + kk);
             const f32x4 a = src[0], b = src[1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = i < 4 ? a[i % 4] : b[i % 4];
-                p[0][i] = to16<DT>(v);
-                const float f1 = widen_bits<DT>(p[0][i]);
-                if (__builtin_isfinite(v) && __builtin_isfinite(f1)) {
-                    const float r1 = v - f1;
-                    p[1][i] = to16<DT>(r1);
-                    p[2][i] = to16<DT>(r1 - widen_bits<DT>(p[1][i]));
-                }
-            }
+            for (int i = 0; i < 8; ++i) s16_split<DT>(i < 4 ? a[i % 4] : b[i % 4], p[0][i], p[1][i], p[2][i]);
         }
         uint8_t* to = packed + unit * 3 * kPartBytes + lane * 16;
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<ds_u32x4*>(to + q * kPartBytes) =
-                ds_u32x4{p[q][0] | p[q][1] << 16, p[q][2] | p[q][3] << 16, p[q][4] | p[q][5] << 16, p[q][6] | p[q][7] << 16};
+            *reinterpret_cast<s16u32x4*>(to + q * kPartBytes) =
+                s16u32x4{p[q][0] | p[q][1] << 16, p[q][2] | p[q][3] << 16, p[q][4] | p[q][5] << 16,
+                         p[q][6] | p[q][7] << 16};
     }
 }
 
@@ -116,7 +83,7 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
                                                                uint32_t n, uint32_t k, uint32_t group_rows,
                                                                uint32_t group_cols, uint32_t groups_down,
                                                                float* __restrict__ out) {
-    __shared__ ds_u32x4 buf[2][2][kTile][4];  // [buffer][step of 32][column][chunk, permuted]
+    __shared__ s16u32x4 buf[2][2][kTile][4];  // [buffer][step of 32][column][chunk, permuted]
     const uint32_t tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tid >> 6));
     // block -> XCD, group of that XCD, tile of the group
@@ -138,27 +105,27 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
     const uint8_t* wsrc = weights + (size_t)min(col0 + wcol, n - 1) * k * 2;
 
     struct Parts {
-        ds_u32x4 p[kWaveRows][3];
+        s16u32x4 p[kWaveRows][3];
     };
     auto load_x = [&](uint32_t step, Parts& x) {  // step past the end: the last one again
         const size_t off = (size_t)min(step, steps - 1) * 3 * kPartBytes;
 #pragma unroll
         for (int t = 0; t < kWaveRows; ++t)
 #pragma unroll
-            for (int p = 0; p < 3; ++p) x.p[t][p] = *reinterpret_cast<const ds_u32x4*>(xrow[t] + off + p * kPartBytes);
+            for (int p = 0; p < 3; ++p) x.p[t][p] = *reinterpret_cast<const s16u32x4*>(xrow[t] + off + p * kPartBytes);
     };
-    ds_u32x4 w[4];
+    s16u32x4 w[4];
     auto load_w = [&](uint32_t pair) {  // steps 2*pair, 2*pair+1; this thread's step is whalf
         const uint32_t c0 = min(pair, steps / 2 - 1) * 8 + whalf * 4;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c)
-            w[c] = *reinterpret_cast<const ds_u32x4*>(wsrc + (size_t)min(c0 + c, chunks - 1) * 16);
+            w[c] = *reinterpret_cast<const s16u32x4*>(wsrc + (size_t)min(c0 + c, chunks - 1) * 16);
     };
     auto store_w = [&](uint32_t pair, uint32_t b) {
         const uint32_t c0 = pair * 8 + whalf * 4;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c)
-            buf[b][whalf][wcol][c ^ place(wcol)] = c0 + c < chunks ? w[c] : ds_u32x4{0, 0, 0, 0};  // zeros past k
+            buf[b][whalf][wcol][c ^ place(wcol)] = c0 + c < chunks ? w[c] : s16u32x4{0, 0, 0, 0};  // zeros past k
     };
 
     f32x4 hi[kWaveRows][kColTiles], lo[kWaveRows][kColTiles];
@@ -185,19 +152,19 @@ __global__ __launch_bounds__(256, 2) void dense_split16_kernel(const uint8_t* __
             const uint32_t s = (2 * half + h2) % kAhead;
 #pragma unroll
             for (int h = 0; h < kColTiles; h += 4) {
-                ds_u32x4 wt[4];
+                s16u32x4 wt[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) wt[c] = buf[b][h2][(h + c) * 16 + i][g ^ place(i)];
 #pragma unroll
                 for (int t = 0; t < kWaveRows; ++t)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) hi[t][h + c] = product<DT>(x[s].p[t][0], wt[c], hi[t][h + c]);
+                    for (int c = 0; c < 4; ++c) hi[t][h + c] = s16_mfma<DT>(x[s].p[t][0], wt[c], hi[t][h + c]);
 #pragma unroll
                 for (int p = 1; p < 3; ++p)
 #pragma unroll
                     for (int t = 0; t < kWaveRows; ++t)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) lo[t][h + c] = product<DT>(x[s].p[t][p], wt[c], lo[t][h + c]);
+                        for (int c = 0; c < 4; ++c) lo[t][h + c] = s16_mfma<DT>(x[s].p[t][p], wt[c], lo[t][h + c]);
             }
             load_x(2 * pair + h2 + kAhead, x[s]);
         }
