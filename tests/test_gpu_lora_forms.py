@@ -81,7 +81,7 @@ def test_projections_beyond_the_small_tiles(lib, dtype, m, n, k, a_dtype):
     the F32 order through eidm_matmul_id, its ids written by the shrink."""
     print(f"[case] {dtype} {m} {n} {k}", flush=True)
     kernels = projection(lib, dtype, m, n, k, B.ARITH_F32, a_dtype).kernels()
-    assert kernels[0] == "lora_shrink" and kernels[-1] == "lora_expand" and "lora_base" not in kernels
+    assert "lora_shrink" in kernels and kernels[-1] == "lora_expand" and "lora_base" not in kernels
     assert kernels[-2].startswith("grouped")
 
 
@@ -94,10 +94,10 @@ SORTED = ["lora_shrink", "lora_expand"]  # behind a map
                                Lora("adapters_65", BF, BF, 1400, 700, 628, 65, 16),
                                Lora("adapters_130", BF, HF, 1200, 577, 431, 130, 33, pad=1),
                                Lora("adapters_300_given", FL, BF, 1200, 830, 996, 300, 24, given=True),
-                               Lora("most_adapters", BF, BF, 2700, 250, 900, 2048, 40),
-                               Lora("most_adapters_f32", FL, FL, 9500, 233, 600, 2048, 9, given=True),
-                               Lora("one_adapter_of_many", BF, BF, 1300, 300, 500, 500, 64, runs=1, none=0.0),
-                               Lora("two_of_many", HF, HF, 1000, 270, 588, 200, 48, runs=3, given=True),
+                               Lora("most_adapters", BF, BF, 4000, 250, 900, 2048, 40),
+                               Lora("most_adapters_f32", FL, FL, 11000, 233, 600, 2048, 9, given=True),
+                               Lora("one_adapter_of_many", BF, BF, 1400, 300, 500, 500, 64, runs=1, none=0.0),
+                               Lora("two_of_many", HF, HF, 1100, 270, 588, 200, 48, runs=3, given=True),
                                Lora("long_k_f32", FL, FL, 37, 63, 16300, 6, 19),
                                Lora("long_k_odd", HF, BF, 70, 77, 16301, 5, 41, pad=1),
                                Lora("long_k_most_ranks", BF, BF, 50, 130, 16264, 3, 256, given=True, ranks=False),
@@ -115,7 +115,7 @@ def test_rows_sorted_over_many_adapters(lib, p):
 
 @pytest.mark.parametrize("m,n,k,adapters,rank,sorts", [
     (200, 128, 512, 2048, 64, False), (200, 128, 512, 256, 64, False), (800, 128, 512, 2048, 16, False),
-    (100, 1024, 1024, 2048, 256, False), (400, 3000, 200, 256, 64, False), (400, 3000, 200, 32, 64, True),
+    (100, 1024, 1024, 2048, 256, False), (400, 3000, 200, 256, 64, True), (400, 3000, 200, 32, 64, True),
     (1600, 4096, 4096, 32, 4, True), (1600, 4096, 4096, 256, 64, True)])
 def test_rows_are_sorted_only_where_that_is_faster(lib, m, n, k, adapters, rank, sorts):
     """A slot per adapter costs more than it saves a few rows of many adapters
