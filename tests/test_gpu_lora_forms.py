@@ -116,7 +116,8 @@ def test_rows_sorted_over_many_adapters(lib, p):
 @pytest.mark.parametrize("m,n,k,adapters,rank,sorts", [
     (200, 128, 512, 2048, 64, False), (200, 128, 512, 256, 64, False), (800, 128, 512, 2048, 16, False),
     (100, 1024, 1024, 2048, 256, False), (400, 3000, 200, 256, 64, True), (400, 3000, 200, 32, 64, True),
-    (1600, 4096, 4096, 32, 4, True), (1600, 4096, 4096, 256, 64, True)])
+    (1600, 4096, 4096, 32, 4, True), (1600, 4096, 4096, 256, 64, True), (8120, 64, 112, 20, 2, True),
+    (2229, 539, 64, 4, 9, True)])
 def test_rows_are_sorted_only_where_that_is_faster(lib, m, n, k, adapters, rank, sorts):
     """A slot per adapter costs more than it saves a few rows of many adapters
     (up to seven times the time); many rows and long ones gain up to half."""
