@@ -476,7 +476,8 @@ class Library:
     def moe_ffn_decode(self, shape: FfnShape, w_gate, w_up, w_down, x, logits, bias, ids, gates, out, scratch,
                        renormalize: bool = True, stream=None) -> None:
         """The expert FFN of up to DECODE_MAX_TOKENS tokens: moe_ffn's results
-        bit for bit, each touched expert's weights read once."""
+        bit for bit, each touched expert's weights read once for up to 16
+        rows (or once per row where that is cheaper)."""
         dev = torch.cuda.current_device()
         m, top_k, f32 = shape.m, shape.top_k, torch.float32
         act, routed = 4 * m * shape.hidden, 4 * m * top_k
