@@ -3,8 +3,8 @@
 //     reduction order), a = the row's adapter;
 //   expand: out[t] = base[t] + scale_a * (B_a v[t]).
 // The shared projection beside them (base = W x), when the call computes it:
-//   * up to four rows, and up to 3 tiles of 32 x 32 outputs a compute unit:
-//     base_few_kernel here, the F32 order;
+//   * up to four rows, and up to 3 tiles of 32 x 32 outputs a compute unit (16
+//     with short k): base_few_kernel here, the F32 order;
 //   * many rows in the split-16 arithmetic: dense_split16.hip;
 //   * else eidm_matmul_id with one expert.  The same bits in each.
 //
@@ -461,12 +461,19 @@ hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t str
 
 // Up to four rows staged in LDS: at any n (k 4096, bf16, us, this : the
 // library's Direct or Grouped kernels: 1 x 32768 45 : 53, 2 x 32768 48 : 77,
-// 4 x 65536 125 : 133; k 512, 4 x 65536 31 : 34). More rows: the Grouped kernels
-// take over where the 32x32 tiles fill the device more than three times (they
-// share activations through LDS).
+// 4 x 65536 125 : 133; k 512, 4 x 65536 31 : 34). More rows: the Grouped kernels,
+// which share activations through LDS, take over where 32x32 tiles fill the
+// device more than three times and long products make up for their map and
+// their other launches (some 9 us). Over 440 products (5 - 16384 rows, 128 - 4096
+// tiles, k 64 - 4096, bf16 and f32) the chosen one takes 0.9 % more than the
+// better one on average, 27 % at most: bf16, 512 x 2048, k 768 35 : 44, k 4096
+// 112 : 110; 1024 x 4096, k 64 31 : 44; 2048 x 1024, k 4096 209 : 194; 512 x 1536,
+// k 4096 72 : 100.
 bool lora_base_few_supported(const LoraArgs& a, int device_cus) {
     if (few_rows_staged(a) && (a.n + 15) / 16 < (1u << 23)) return true;  // (a grid of below 2^32 threads)
-    return ((uint64_t)a.m + 31) / 32 * ((a.n + 31) / 32) <= (uint64_t)device_cus * 3;
+    const uint64_t cus = device_cus > 0 ? (uint64_t)device_cus : 256;
+    const uint64_t tiles = ((uint64_t)a.m + 31) / 32 * (((uint64_t)a.n + 31) / 32);
+    return tiles <= cus * 3 || (tiles <= cus * 16 && tiles * ((uint64_t)a.k + 500) <= cus * 23400);
 }
 
 hipError_t launch_lora_base_few(const LoraArgs& a, int weight_dtype, const uint8_t* weights, int device_cus,

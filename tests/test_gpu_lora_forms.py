@@ -74,11 +74,20 @@ def test_projection_tiles_are_spread_over_all_xcds(lib, dtype, m, n, k):
     assert receipt.launches[receipt.recorded - 2].grid in {-(-t // 8) * 8 for t in tiles}
 
 
-@pytest.mark.parametrize("dtype,m,n,k,a_dtype", [(BF, 900, 1003, 137, None), (HF, 1031, 2000, 264, FL), (FL, 512, 2048, 300, None),
-                                                 (BF, 512, 4096, 1024, None), (BF, 5, 131072, 64, None)])
+@pytest.mark.parametrize("dtype,m,n,k", [(BF, 900, 1003, 137), (HF, 1031, 2000, 264), (FL, 512, 2048, 300), (BF, 512, 4096, 1024),
+                                         (BF, 5, 131000, 64), (HF, 16384, 75, 130), (FL, 2048, 2040, 65)])
+def test_many_small_tiles_of_short_products(lib, dtype, m, n, k):
+    """Up to 16 tiles of 32 x 32 a compute unit where k is short (up to twice as
+    fast as the gathered kernels with their map)."""
+    print(f"[case] {dtype} {m} {n} {k}", flush=True)
+    assert "lora_base" in projection(lib, dtype, m, n, k, B.ARITH_F32).kernels()
+
+
+@pytest.mark.parametrize("dtype,m,n,k,a_dtype", [(BF, 4100, 1030, 137, None), (HF, 4200, 1000, 264, FL), (FL, 512, 2048, 6001, None),
+                                                 (BF, 512, 4096, 3000, None), (BF, 5, 131104, 64, None)])
 def test_projections_beyond_the_small_tiles(lib, dtype, m, n, k, a_dtype):
-    """More than three 32 x 32 tiles a compute unit, the ordinary prompt chunk:
-    the F32 order through eidm_matmul_id, its ids written by the shrink."""
+    """Long products of more than three 32 x 32 tiles a compute unit, the ordinary
+    prompt chunk: the F32 order through eidm_matmul_id, its ids written by the shrink."""
     print(f"[case] {dtype} {m} {n} {k}", flush=True)
     kernels = projection(lib, dtype, m, n, k, B.ARITH_F32, a_dtype).kernels()
     assert "lora_shrink" in kernels and kernels[-1] == "lora_expand" and "lora_base" not in kernels
