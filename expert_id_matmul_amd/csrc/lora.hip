@@ -436,18 +436,19 @@ hipError_t expand_dt(const LoraArgs& a, int device_cus, hipStream_t stream) {
 }  // namespace
 
 // By rows, every row reads its own adapter; sorted, there are a map and a slot
-// per adapter, whether it has rows or not, in both launches. Over 1560 calls
-// (m 64 - 4000, n + k 640 - 8192, rank 4 - 256, 4 - 2048 adapters, with a
-// projection beside them and on given rows, scattered ids and runs) the chosen
-// form takes 0.8 % more than the better one on average. Given rows, bf16, us,
+// per adapter, whether it has rows or not, in both launches. A row weighs its
+// adapter's bytes, B's short rows three times A's, and a part of its own. Over
+// 2260 calls (65 - 8192 rows, rank 1 - 256, 1 - 2048 adapters, with a projection
+// beside them and on given rows, scattered ids and runs) the chosen form takes
+// 0.9 % more than the better one on average, 60 % at most. Given rows, bf16, us,
 // by rows : sorted: 200 x 128 x 512, rank 64, 32 adapters 12 : 18, 256 adapters
 // 12 : 22, 2048 adapters 13 : 77; 400 x 3000 x 200, rank 64, 256 adapters 55 : 28;
 // 1600 x 4096 x 4096, rank 4, 32 adapters 58 : 31; rank 64, 2048 adapters 262 : 135.
 bool lora_sorts_rows(uint32_t m, uint32_t n, uint32_t k, uint32_t n_adapters, uint32_t max_rank) {
     if (!stages_rows(1, k)) return true;  // the row form stages a row
-    const double read = m * ((max_rank + 8) * (2.0 * n + k) + 20e3);  // B's short rows weigh twice A's
+    const double rows = m * ((max_rank + 8) * (3.0 * n + k) + 15e3);
     const double slots = (double)n_adapters * ((max_rank + 31) / 32 + (n + 255) / 256);  // blocks of empty slots
-    return m > kLoraRowForm && read > 55e6 + 32e3 * slots;
+    return m > kLoraRowForm && rows > 70e6 + 24e3 * slots;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& a, int device_cus, hipStream_t stream) {

@@ -485,7 +485,9 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
  * scratch       device, 256-byte aligned, at least
  *               eidm_lora_linear_scratch_bytes(shape) bytes (which count the
  *               shared projection's; the shape's weight_dtype and arith must
- *               be valid for that call); its contents need no preparation
+ *               be valid for that call, and a shape that is only used with a
+ *               base is smallest with EIDM_ARITH_F32); its contents need no
+ *               preparation
  *               and mean nothing afterwards, and calls that may overlap in
  *               time need one each
  * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m, n and k as
