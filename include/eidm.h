@@ -487,9 +487,8 @@ int eidm_moe_ffn_decode(const eidm_ffn_shape* shape, const void* w_gate, const v
  *               shared projection's; the shape's weight_dtype and arith must
  *               be valid for that call, and a shape that is only used with a
  *               base is smallest with EIDM_ARITH_F32); its contents need no
- *               preparation
- *               and mean nothing afterwards, and calls that may overlap in
- *               time need one each
+ *               preparation and mean nothing afterwards, and calls that may
+ *               overlap in time need one each
  * Limits: n_adapters <= 2048, max_rank <= EIDM_LORA_MAX_RANK, m, n and k as
  * for eidm_matmul_id, and fewer than 2^32 threads a launch (else
  * EIDM_E_UNSUPPORTED): where rows are sorted by adapter (with k above 16256,
