@@ -12,6 +12,8 @@
 //              + (e is pick j) d_gates[t, j], or with renormalised gates
 //                (d_gates[t, j] - sum_i d_gates[t, i] * gates[t, i]) / sum_i s[t, ids[t, i]]
 //   d_logits   = d_s * s * (1 - s)
+// Renormalised gates are ratios, of order one beside the smallest scores: those
+// of tiny scores, and their gradients, come from the logits' differences.
 //
 // Bound by memory beyond a few thousand tokens (the logits once, their
 // gradient once): a wavefront takes a token, its scores and its experts' sums
@@ -59,20 +61,21 @@ __device__ __forceinline__ void seq_range(const BalanceArgs& a, uint32_t q, uint
     hi = a.seq_offsets ? max(min(a.seq_offsets[q + 1], a.m), lo) : a.m;
 }
 
-// exp(-|v|): the argument's product with log2(e) in two parts, so that the
-// error stays at an f32 rounding or two for any |v| (one product would lose
-// |v| of them).  v_exp_f32 flushes what falls below 2^-126, an infinite logit's
-// (of a masked expert) like that of -256; a NaN stays one.
-__device__ __forceinline__ float exp_minus_abs(float v) {
-    const float x = __builtin_elementwise_maximum(-fabsf(v), -256.0f), hi = x * 0x1.715476p+0f;
+// exp(x + rest), x <= 0 and rest a rounding of it: the argument's product with
+// log2(e) in two parts, so that the error stays at an f32 rounding or two for
+// any x (one product would lose |x| of them).  v_exp_f32 flushes what falls
+// below 2^-126, an infinite x like -256; a NaN stays one.
+__device__ __forceinline__ float exp_below(float x, float rest = 0.0f) {
+    x = __builtin_elementwise_maximum(x, -256.0f);
+    const float hi = x * 0x1.715476p+0f;
     const float lo = __builtin_fmaf(x, 0x1.4ae0cp-26f, __builtin_fmaf(x, 0x1.715476p+0f, -hi));
     const float e = __builtin_amdgcn_exp2f(hi);
-    return __builtin_fmaf(e, lo * 0x1.62e43p-1f, e);
+    return __builtin_fmaf(e, __builtin_fmaf(lo, 0x1.62e43p-1f, rest), e);
 }
 
 // s = sigmoid(v) and s * (1 - s), without a difference that cancels.
 __device__ __forceinline__ void score(float v, float& s, float& slope) {
-    const float t = exp_minus_abs(v), r = __builtin_amdgcn_rcpf(1.0f + t);
+    const float t = exp_below(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + t);
     s = v >= 0.0f ? r : t * r;
     slope = t * r * r;
 }
@@ -93,6 +96,31 @@ __device__ __forceinline__ float wave_sum_f(float v) {
     v += dpp_f<0x140>(v);
     return (lane_f(v, 0) + lane_f(v, 16)) + (lane_f(v, 32) + lane_f(v, 48));
 }
+
+__device__ __forceinline__ float wave_max_f(float v) {  // a NaN is the largest
+    v = __builtin_elementwise_maximum(v, dpp_f<0xb1>(v));
+    v = __builtin_elementwise_maximum(v, dpp_f<0x4e>(v));
+    v = __builtin_elementwise_maximum(v, dpp_f<0x141>(v));
+    v = __builtin_elementwise_maximum(v, dpp_f<0x140>(v));
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(lane_f(v, 0), lane_f(v, 16)),
+                                         __builtin_elementwise_maximum(lane_f(v, 32), lane_f(v, 48)));
+}
+
+// Where a sum of scores is below this, each is its logit's exponential (1 - s is
+// 1 to 2^-28), and ratios of them are taken from the differences to the largest
+// logit: the scores themselves are flushed below 2^-126.
+constexpr float kTiny = 0x1p-28f;
+
+// sigmoid(v) / sigmoid(most) for v <= most, both tiny; the difference's own rounding
+// is added to it.
+__device__ __forceinline__ float score_beside(float v, float most) {
+    v = __builtin_elementwise_maximum(v, -512.0f);
+    const float d = v - most;
+    return exp_below(d, -most - (d - v));
+}
+
+// The largest logit whose score is 0 in f32: half of the smallest number, -150 ln 2.
+constexpr float kNoScore = -0x1.9fe36ap+6f;
 
 // Expert of a lane's slot v: runs of up to four neighbours, one load each.
 template <int NV>
@@ -296,7 +324,7 @@ __global__ __launch_bounds__(kFinish) void balance_finish_kernel(BalanceArgs a) 
 // A wavefront takes a stretch of tokens, so that a sequence's loads are fetched once for all of it.
 template <int NV>
 __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(BalanceArgs a, uint32_t each) {
-    __shared__ float picks[kWaves][64 * NV];  // a token's gradients of its picks' scores, zeros between tokens
+    __shared__ float picks[kWaves][64 * NV];  // a token's gradients of its picks' logits, zeros between tokens
     const uint32_t lane = threadIdx.x & 63, n = a.n_experts, k = a.top_k;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const uint64_t first = ((uint64_t)blockIdx.x * kWaves + wave) * each;
@@ -356,37 +384,42 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(BalanceArgs
             Experts<NV>::store(a.d_logits + (size_t)t * n, n, d);
             continue;
         }
-        float s[NV], slope[NV];
-        if (id < n) {
-            float unused;
-            score(next_logit, picked, unused);
-        } else {
-            dg = 0.0f;
-        }
+        float s[NV], slope[NV], by = 0.0f;  // by: what the pick's gradient comes to its logit with
+        if (id < n) score(next_logit, picked, by);
+        else dg = 0.0f;
         const float r = scores<NV>(l, n, s, slope);
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) dot += load[v] * s[v];
         dot = wave_sum_f(dot) * r;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) d[v] = w * (load[v] - dot) * r;
+        for (int v = 0; v < NV; ++v) d[v] = w * (load[v] - dot) * r * slope[v];
         if (a.d_gates) {
             if (a.renormalize) {
                 // by the gates themselves: the only pick of a token has 1, and exactly no gradient
-                const float of = wave_sum_f(picked), inv = of < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(of);
-                const float gate = of < 0x1p-126f ? 0.0f : __fdiv_rn(picked, of);
-                dg = (dg - wave_sum_f(dg * gate)) * inv;
+                const float of = wave_sum_f(picked);
+                float gate = 0.0f;
+                if (!(of < kTiny)) {
+                    gate = __fdiv_rn(picked, of);
+                    by *= __builtin_amdgcn_rcpf(of);
+                } else {
+                    const float most = wave_max_f(id < n ? next_logit : -__builtin_inff());
+                    if (most > kNoScore) {
+                        const float p = id < n ? score_beside(next_logit, most) : 0.0f;
+                        gate = __fdiv_rn(p, wave_sum_f(p));
+                    }
+                    by = gate;
+                }
+                dg -= wave_sum_f(dg * gate);
             }
             // the wavefront's own LDS row, in program order: no barrier
-            if (id < n) atomicAdd(&mine[id], dg);
+            if (id < n) atomicAdd(&mine[id], dg * by);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
             for (int v = 0; v < NV; ++v) d[v] += mine[Experts<NV>::of(v)];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (id < n) mine[id] = 0.0f;
         }
-#pragma unroll
-        for (int v = 0; v < NV; ++v) d[v] *= slope[v];
         Experts<NV>::store(a.d_logits + (size_t)t * n, n, d);
     }
 }

@@ -608,6 +608,8 @@ int eidm_matmul_id_i8(const eidm_i8_shape* shape, int route, const int8_t* weigh
  *   y = the 8-bit products with W_down                  (eidm_matmul_id_i8)
  *   out = combine(y, gates)                             (eidm_combine)
  * Both routes have the same bits, and a token's results depend on no other.
+ * A token without a score (eidm_route_backward) has a row of NaN when its gates
+ * are renormalised, of zeros when not.
  * w_gate, w_up     device [n_experts][inter][hidden] at gate_up_stride_bytes an
  *                  expert (one extent, gate_up_bytes, vouched for both);
  *                  gate_scales, up_scales f32 [n_experts, inter]
@@ -768,6 +770,11 @@ int eidm_route_balance(const eidm_balance_shape* shape, const float* logits, con
  * The gradient of the router's logits through its gates (eidm_route_topk) and
  * through the balance loss (eidm_route_balance; its counts are constant).
  * The selection has no gradient, nor has the selection bias.
+ * Renormalised gates have theirs however small the scores.  Where the f32
+ * scores of all of a token's picks are 0 (logits below about -103.97: a token
+ * of masked experts alone) eidm_route_topk's gates are NaN, which makes the
+ * token's row of any output that takes them NaN, and here nothing comes
+ * through them: zeros.
  * counts      eidm_route_balance's
  * d_gates     device f32 [m, top_k], or NULL: none (eidm_block_norm_backward's
  *             d_slot_gates, where the experts' slots are weighted there)

@@ -1,0 +1,87 @@
+"""The router's gradient and balance loss at the ends of the scores' range and
+of the calls' sizes, on the GPU against the formulas in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from expert_id_matmul_amd import binding as B
+from test_gpu_balance import DEPTH, SCORE, SLOPE, ULP, Case
+from test_gpu_ffn_i8 import Ffn
+
+pytestmark = pytest.mark.gpu
+
+# of a gate's gradient through renormalised gates: a gate is a score over a sum of them (2 * SCORE + 8), the differences
+# of d_gates 1, their weighted sum 8, the factor score * (1 - score) / sum at most SCORE + 2 * SLOPE, four steps between
+GATES = 2 * (2 * SCORE + 8) + SCORE + 2 * SLOPE + 16
+
+
+def chosen(c, logits):
+    c.logits = logits
+    c.ids = torch.topk(logits, c.k, dim=1).indices.int()
+    return c
+
+
+def near(got, want, bound):
+    off = (got.double() - want).abs()
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+def test_gates_of_tiny_scores_have_their_gradient(lib):
+    """Renormalised gates are ratios: they and their gradient are of order one however small the scores."""
+    c = Case(lib, 64, 40, 4, None, True, 1.0)
+    g = torch.Generator().manual_seed(8)
+    least = torch.rand(64, 1, generator=g) * 80 + 20  # each token's largest logit from -20 down to -100
+    chosen(c, (-least - 3 * torch.rand(64, 40, generator=g)).clamp(min=-103.5))
+    c.logits[::5, ::3] -= 60  # beside experts far below
+    chosen(c, c.logits)
+    got = c.backward(c.forward()[0], loss=False)
+    _, _, _, want, size = c.formula(loss=False)
+    assert want.abs().max(1).values.min() > 1e-3
+    near(got, want, GATES * ULP * size + 1e-30)
+
+
+def test_gates_without_a_score_have_no_gradient(lib):
+    """The router's scores are f32: below about -103.97 they are 0, and where all picks' are, no gate is a number."""
+    c = Case(lib, 12, 40, 4, None, True, 1.0)
+    c.logits[3], c.logits[5], c.logits[7] = -104.0, float("-inf"), -1e30
+    c.logits[8] = -103.9
+    chosen(c, c.logits)
+    got = c.backward(c.forward()[0], loss=False)
+    assert torch.isfinite(got).all() and (got[[3, 5, 7]] == 0).all()
+    d = c.d_gates[8].double()
+    near(got[8, c.ids[8].long()], (d - d.mean()) / 4, GATES * ULP * d.abs().sum())
+
+
+def test_a_pick_that_is_no_number_stays_in_its_token(lib):
+    c = Case(lib, 12, 40, 4, None, True, 1.0)
+    counts = c.forward()[0]
+    want = c.backward(counts)
+    for value in (float("nan"), -90.0):
+        other = -90.0 if value != value else float("nan")
+        c.logits[6, c.ids[6, :3].long()] = value
+        c.logits[6, c.ids[6, 3].long()] = other
+        got = c.backward(counts)
+        assert torch.isnan(got[6, c.ids[6].long()]).all()
+        rest = torch.arange(12) != 6
+        assert torch.equal(got[rest], want[rest])
+
+
+@pytest.mark.parametrize("m,hidden", [(1, 96), (12, 96), (12, 9000)], ids=["one", "one_launch", "start"])
+@pytest.mark.parametrize("renormalize", [True, False], ids=["renormalised", "as_they_are"])
+def test_a_token_of_masked_experts_alone(lib, m, hidden, renormalize):
+    """No score: NaN gates and a row of NaN where the gates are renormalised, zeros where not, and no other row's matter;
+    the gradient through its gates is zero."""
+    c = Ffn(lib, m, hidden, 64, 3, 6, True, renormalize)
+    clean = {r: c.result(r) for r in (B.DIRECT, B.GROUPED)}
+    masked = m // 2
+    for value in (float("-inf"), -104.0):
+        c.logits[masked] = value
+        for r, want in clean.items():
+            got = c.result(r)
+            assert np.isnan(got[masked]).all() if renormalize else (got[masked] == 0).all()
+            np.testing.assert_array_equal(np.delete(got, masked, 0), np.delete(want, masked, 0))
+            assert (c.ids.cpu() >= 0).all() and (c.ids.cpu() < 6).all()
+        d = torch.full((m, 6), float("nan"), device="cuda")
+        lib.route_backward(B.make_balance_shape(m, 6, 3), c.logits, c.ids, None, torch.ones(1, 6, dtype=torch.int32).cuda(),
+                           torch.ones(m, 3).cuda(), None, d, renormalize=renormalize)
+        assert (d[masked] == 0).all() and torch.isfinite(d).all()
