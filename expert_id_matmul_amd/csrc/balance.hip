@@ -396,7 +396,6 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(BalanceArgs
         for (int v = 0; v < NV; ++v) d[v] = w * (load[v] - dot) * r * slope[v];
         if (a.d_gates) {
             if (a.renormalize) {
-                // by the gates themselves: the only pick of a token has 1, and exactly no gradient
                 const float of = wave_sum_f(picked);
                 float gate = 0.0f;
                 if (!(of < kTiny)) {
@@ -410,6 +409,9 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(BalanceArgs
                     }
                     by = gate;
                 }
+                // by the differences from the gate that has most of the weight, if one has: its own gradient is small
+                // beside d_gates, and the difference that leaves it would cancel
+                if (const uint64_t large = __ballot(gate > 0.5f)) dg -= lane_f(dg, __builtin_ctzll(large));
                 dg -= wave_sum_f(dg * gate);
             }
             // the wavefront's own LDS row, in program order: no barrier

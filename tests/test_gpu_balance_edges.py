@@ -85,3 +85,22 @@ def test_a_token_of_masked_experts_alone(lib, m, hidden, renormalize):
         lib.route_backward(B.make_balance_shape(m, 6, 3), c.logits, c.ids, None, torch.ones(1, 6, dtype=torch.int32).cuda(),
                            torch.ones(m, 3).cuda(), None, d, renormalize=renormalize)
         assert (d[masked] == 0).all() and torch.isfinite(d).all()
+
+
+def test_a_gate_beside_tiny_ones_has_its_gradient(lib):
+    """d_gates[j] less the weighted mean of them all, where one gate has nearly all the weight: the sum of the differences
+    from that gate's, in which nothing cancels."""
+    c = Case(lib, 64, 40, 4, None, True, 1.0)
+    g = torch.Generator().manual_seed(9)
+    logits = -14 - 4 * torch.rand(64, 40, generator=g)
+    logits[torch.arange(64), torch.randint(0, 40, (64,), generator=g)] = 2 * torch.randn(64, generator=g)
+    chosen(c, logits)
+    c.ids = c.ids[:, torch.randperm(4, generator=g)].contiguous()  # with a selection bias the largest score is anywhere
+    got = c.backward(c.forward()[0], loss=False)
+    _, _, _, want, _ = c.formula(loss=False)
+    at, d = c.ids.long(), c.d_gates.double()
+    s = torch.sigmoid(torch.gather(c.logits.double(), 1, at))
+    gate, top = s / s.sum(1, keepdim=True), s.argmax(1, keepdim=True)
+    off = (d - torch.gather(d, 1, top)).abs()
+    size = torch.zeros(64, 40, dtype=torch.float64).scatter_(1, at, gate * (1 - s) * (off + (gate * off).sum(1, keepdim=True)))
+    near(got, want, GATES * ULP * size)
