@@ -121,6 +121,8 @@ __device__ __forceinline__ float score_beside(float v, float most) {
 
 // The largest logit whose score is 0 in f32: half of the smallest number, -150 ln 2.
 constexpr float kNoScore = -0x1.9fe36ap+6f;
+// The largest whose score is not above 2^-126, -126 ln 2.
+constexpr float kLeastScore = -0x1.5d58ap+6f;
 
 // Expert of a lane's slot v: runs of up to four neighbours, one load each.
 template <int NV>
@@ -155,7 +157,9 @@ struct Experts {
 };
 
 // A token's scores (0 past n_experts) and the factor that makes them
-// probabilities: 0 where no score is left above the smallest normal number.
+// probabilities.  Scores that are all tiny become their ratios to the largest,
+// with a slope of the same (1 - s is 1): what follows takes them times that
+// factor alone.  Where the largest itself is not above 2^-126 all are 0.
 template <int NV>
 __device__ __forceinline__ float scores(const float (&l)[NV], uint32_t n, float (&s)[NV], float (&slope)[NV]) {
     float total = 0.0f;
@@ -166,7 +170,23 @@ __device__ __forceinline__ float scores(const float (&l)[NV], uint32_t n, float 
         total += s[v];
     }
     total = wave_sum_f(total);
-    return total < 0x1p-126f ? 0.0f : __builtin_amdgcn_rcpf(total);
+    if (total < kTiny) {
+        float most = -__builtin_inff();
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (Experts<NV>::of(v) < n) most = fmaxf(most, l[v]);
+        most = wave_max_f(most);
+        total = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            s[v] = most > kLeastScore && Experts<NV>::of(v) < n ? score_beside(l[v], most) : 0.0f;
+            slope[v] = s[v];
+            total += s[v];
+        }
+        total = wave_sum_f(total);
+        if (total == 0.0f) return 0.0f;
+    }
+    return __builtin_amdgcn_rcpf(total);
 }
 
 constexpr int kWaves = 4;      // of a block of the gradient

@@ -104,3 +104,20 @@ def test_a_gate_beside_tiny_ones_has_its_gradient(lib):
     off = (d - torch.gather(d, 1, top)).abs()
     size = torch.zeros(64, 40, dtype=torch.float64).scatter_(1, at, gate * (1 - s) * (off + (gate * off).sum(1, keepdim=True)))
     near(got, want, GATES * ULP * size)
+
+
+@pytest.mark.parametrize("experts", [40, 700])
+def test_probabilities_of_tiny_scores(lib, experts):
+    """A token whose largest score is near the smallest number has probabilities like any other."""
+    c = Case(lib, 50, experts, 3, [0, 20, 50], True, 1.0)
+    g = torch.Generator().manual_seed(10)
+    logits = -84 - 8 * torch.rand(50, experts, generator=g)
+    logits[::2] += 55 * torch.rand(25, 1, generator=g)
+    chosen(c, logits)
+    assert (c.logits.max(1).values > -87).all() and (c.logits.min(1).values < -87.4).any()
+    counts, mean, loss = c.forward()
+    _, want_mean, want_loss, want, size = c.formula(gates=False)
+    bound = (2 * SCORE + DEPTH + 3 + c.m) * ULP
+    near(mean.view(2, -1), want_mean, bound * want_mean)
+    assert abs(float(loss) - want_loss) <= bound * want_loss
+    near(c.backward(counts, gates=False), want, (4 * SCORE + 3 * DEPTH + SLOPE + 8) * ULP * size)
