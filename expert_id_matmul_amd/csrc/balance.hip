@@ -589,12 +589,13 @@ int eidm_route_backward(const eidm_balance_shape* shape, const float* logits, co
     a.d_gates = d_gates;
     a.d_loss = d_loss;
     a.d_logits = d_logits;
-    // stretches of up to 16 tokens, shorter while the device is not full (8 wavefronts a SIMD)
-    const uint64_t fill = (uint64_t)device_cus() * 32;
+    // stretches of up to 16 tokens, shorter while the device is not full (8 wavefronts a SIMD), longer
+    // where the launch would have 2^32 threads
+    const uint64_t fill = (uint64_t)device_cus() * 32, most = (1ull << 32) / 64 - kWaves;
     uint64_t each = (a.m + fill - 1) / fill;
     if (each > 16) each = 16;
+    if ((a.m + each - 1) / each > most) each = (a.m + most - 1) / most;
     const uint64_t waves = (a.m + each - 1) / each, grid = (waves + kWaves - 1) / kWaves;
-    if (grid * 64 * kWaves >= 1ull << 32) return api_fail(EIDM_E_UNSUPPORTED, "m too large");
     const hipError_t err = by_width(a.n_experts, [&](auto width) {
         hipLaunchKernelGGL((route_backward_kernel<decltype(width)::value>), dim3((uint32_t)grid), dim3(64 * kWaves), 0,
                            static_cast<hipStream_t>(stream), a, (uint32_t)each);

@@ -121,3 +121,19 @@ def test_probabilities_of_tiny_scores(lib, experts):
     near(mean.view(2, -1), want_mean, bound * want_mean)
     assert abs(float(loss) - want_loss) <= bound * want_loss
     near(c.backward(counts, gates=False), want, (4 * SCORE + 3 * DEPTH + SLOPE + 8) * ULP * size)
+
+
+def test_more_than_2_to_the_30_tokens(lib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 20 * 2 ** 30:
+        pytest.skip("not 20 GiB of device memory free")
+    m = 2 ** 30 + 12345
+    torch.manual_seed(3)
+    logits, d_gates = torch.empty(m, 1, device="cuda").normal_(), torch.empty(m, 1, device="cuda").normal_()
+    ids, counts = torch.zeros(m, 1, dtype=torch.int32, device="cuda"), torch.full((1, 1), m, dtype=torch.int32, device="cuda")
+    got = torch.full((m, 1), float("nan"), device="cuda")
+    lib.route_backward(B.make_balance_shape(m, 1, 1), logits, ids, None, counts, d_gates, None, got, renormalize=False)
+    for lo in range(0, m, 1 << 26):
+        s = torch.sigmoid(logits[lo:lo + (1 << 26)].double())
+        want = d_gates[lo:lo + (1 << 26)].double() * s * torch.sigmoid(-logits[lo:lo + (1 << 26)].double())
+        assert ((got[lo:lo + (1 << 26)].double() - want).abs() <= (SLOPE + 2) * ULP * want.abs() + 1e-30).all()
