@@ -27,8 +27,8 @@
 namespace eidm {
 namespace {
 
-// Blocks below `tokens` (m, or 0 with x in 8 bits already): a token's x to 8
-// bits; the blocks after them: four tokens' routing.
+// Blocks below `quantising` (0 with x in 8 bits already): a token's x to 8 bits;
+// the blocks after them: four tokens' routing.  Either kind takes tokens in turn.
 template <int NV>
 __global__ __launch_bounds__(256) void i8_ffn_start_kernel(const float* __restrict__ logits,
                                                            const float* __restrict__ bias, uint32_t m,
@@ -36,50 +36,53 @@ __global__ __launch_bounds__(256) void i8_ffn_start_kernel(const float* __restri
                                                            uint32_t* __restrict__ ids, float* __restrict__ gates,
                                                            const float* __restrict__ x, uint32_t hidden,
                                                            int8_t* __restrict__ q, float* __restrict__ scales,
-                                                           uint32_t tokens) {
+                                                           uint32_t quantising) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (blockIdx.x >= tokens) {
-        const uint32_t t = (blockIdx.x - tokens) * 4 + wave;
-        if (t >= m) return;
-        uint32_t id;
-        float gate;
-        route_token<NV>(logits + (size_t)t * n_experts, bias, n_experts, top_k, renormalize, id, gate);
-        if (lane < top_k) {
-            ids[(size_t)t * top_k + lane] = id;
-            gates[(size_t)t * top_k + lane] = gate;
+    if (blockIdx.x >= quantising) {
+        const uint32_t each = (gridDim.x - quantising) * 4;
+        for (uint32_t t = (blockIdx.x - quantising) * 4 + wave; t < m; t += each) {
+            uint32_t id;
+            float gate;
+            route_token<NV>(logits + (size_t)t * n_experts, bias, n_experts, top_k, renormalize, id, gate);
+            if (lane < top_k) {
+                ids[(size_t)t * top_k + lane] = id;
+                gates[(size_t)t * top_k + lane] = gate;
+            }
         }
         return;
     }
     __shared__ uint32_t part[4];
-    const uint32_t t = blockIdx.x;
     constexpr uint32_t kHeld = 4;  // units of 8 a thread holds; longer rows are read twice
-    const uint8_t* row = reinterpret_cast<const uint8_t*>(x + (size_t)t * hidden);
-    float v[kHeld][8];
-    uint32_t most = 0;
+    for (uint32_t t = blockIdx.x; t < m; t += quantising) {
+        const uint8_t* row = reinterpret_cast<const uint8_t*>(x + (size_t)t * hidden);
+        float v[kHeld][8];
+        uint32_t most = 0;
 #pragma unroll
-    for (uint32_t u = 0; u < kHeld; ++u) {
-        load_row<kDtypeF32, 8>(row, min((u * 256 + threadIdx.x) * 8, hidden), hidden, v[u]);
+        for (uint32_t u = 0; u < kHeld; ++u) {
+            load_row<kDtypeF32, 8>(row, min((u * 256 + threadIdx.x) * 8, hidden), hidden, v[u]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most = max(most, magnitude(v[u][j]));
-    }
-    for (uint32_t i = (kHeld * 256 + threadIdx.x) * 8; i < hidden; i += 2048) {
-        float w[8];
-        load_row<kDtypeF32, 8>(row, i, hidden, w);
+            for (int j = 0; j < 8; ++j) most = max(most, magnitude(v[u][j]));
+        }
+        for (uint32_t i = (kHeld * 256 + threadIdx.x) * 8; i < hidden; i += 2048) {
+            float w[8];
+            load_row<kDtypeF32, 8>(row, i, hidden, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most = max(most, magnitude(w[j]));
-    }
-    most = wave_max_u32(most);
-    if (lane == 0) part[wave] = most;
-    __syncthreads();
-    const RowScale s = row_scale(max(max(part[0], part[1]), max(part[2], part[3])));
-    if (threadIdx.x == 0) scales[t] = s.scale;
-    int8_t* to = q + (size_t)t * hidden;
+            for (int j = 0; j < 8; ++j) most = max(most, magnitude(w[j]));
+        }
+        most = wave_max_u32(most);
+        if (lane == 0) part[wave] = most;
+        __syncthreads();
+        const RowScale s = row_scale(max(max(part[0], part[1]), max(part[2], part[3])));
+        if (threadIdx.x == 0) scales[t] = s.scale;
+        int8_t* to = q + (size_t)t * hidden;
 #pragma unroll
-    for (uint32_t u = 0; u < kHeld; ++u) store_q(to, min((u * 256 + threadIdx.x) * 8, hidden), hidden, v[u], s);
-    for (uint32_t i = (kHeld * 256 + threadIdx.x) * 8; i < hidden; i += 2048) {
-        float w[8];
-        load_row<kDtypeF32, 8>(row, i, hidden, w);
-        store_q(to, i, hidden, w, s);
+        for (uint32_t u = 0; u < kHeld; ++u) store_q(to, min((u * 256 + threadIdx.x) * 8, hidden), hidden, v[u], s);
+        for (uint32_t i = (kHeld * 256 + threadIdx.x) * 8; i < hidden; i += 2048) {
+            float w[8];
+            load_row<kDtypeF32, 8>(row, i, hidden, w);
+            store_q(to, i, hidden, w, s);
+        }
+        if (quantising < m) __syncthreads();  // the next token's maxima
     }
 }
 
@@ -137,10 +140,13 @@ bool direct_grid_fits(const eidm_ffn_i8_shape* s) {
 // Routing, and x (if it is given) to 8 bits.
 int launch_start(const eidm_ffn_i8_shape* s, const float* logits, const float* bias, int renormalize, uint32_t* ids,
                  float* gates, const float* x, int8_t* q, float* scales, hipStream_t st) {
-    const uint32_t tokens = x ? s->m : 0, grid = tokens + (s->m + 3) / 4, nv = (s->n_experts + 63) / 64;
+    // a token or four to a block while the launch has fewer than 2^32 threads
+    constexpr uint32_t kMost = 1u << 22;
+    const uint32_t quantising = x ? (s->m < kMost ? s->m : kMost) : 0, fours = (s->m + 3) / 4;
+    const uint32_t grid = quantising + (fours < kMost ? fours : kMost), nv = (s->n_experts + 63) / 64;
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, logits, bias, s->m, s->n_experts, s->top_k, renormalize,
-                           ids, gates, x, s->hidden, q, scales, tokens);
+                           ids, gates, x, s->hidden, q, scales, quantising);
     };
     if (nv <= 1) go(i8_ffn_start_kernel<1>);
     else if (nv <= 2) go(i8_ffn_start_kernel<2>);
@@ -197,7 +203,6 @@ int eidm_moe_ffn_i8(const eidm_ffn_i8_shape* shape, int route, const int8_t* w_g
         return api_fail(EIDM_E_INVALID, "unknown route %d", route);
     if (route == EIDM_ROUTE_DIRECT && (s->top_k > kI8DownTopK || !direct_grid_fits(s)))
         return api_fail(EIDM_E_UNSUPPORTED, "the Direct form takes top_k <= %u and fewer than 2^32 threads", kI8DownTopK);
-    if (((uint64_t)s->m + ((uint64_t)s->m + 3) / 4) * 256 >= 1ull << 32) return api_fail(EIDM_E_UNSUPPORTED, "m too large");
     const bool direct = route == EIDM_ROUTE_DIRECT || (route == EIDM_ROUTE_AUTO && ffn_i8_direct(s) && direct_grid_fits(s));
 
     hipStream_t st = static_cast<hipStream_t>(stream);
