@@ -54,6 +54,7 @@ struct NormArgs {
     const float *d_out, *d_normed;
     float *d_x, *d_z, *d_slot_gates, *d_gate;
     float* partial;  // [blocks][3][hidden]: column sums of d_w_pre, d_w_post, d_gate
+    float* rest;     // [blocks][hidden] of the rows read twice: a row's d_z less what is stored of it
     uint32_t sums;   // which of the three are wanted (bits)
 };
 
@@ -557,15 +558,20 @@ __global__ __launch_bounds__(kLongBlock) void block_norm_long_kernel(NormArgs a)
 // ---------------------------------------------------------------- backward
 // d_slot_gates of a row, four slots a reduction; y's row comes from the L2 once
 // more.  part(s, dot): adds a thread's share of slots s .. s+3 to dot.
+template <typename Rows>
+__device__ __forceinline__ void slot_sums(const NormArgs& a, Rows& rows, size_t t, bool live, uint32_t s0, double (&dot)[4]) {
+    rows.sum(dot);
+#pragma unroll
+    for (uint32_t s = 0; s < 4; ++s)
+        if (live && threadIdx.x % Rows::kGroup == 0 && s0 + s < a.top_k) a.d_slot_gates[t * a.top_k + s0 + s] = (float)dot[s];
+}
+
 template <typename Rows, typename PartOf>
-__device__ __forceinline__ void slot_gradients(const NormArgs& a, Rows& rows, size_t t, bool live, PartOf part) {
-    for (uint32_t s0 = 0; s0 < a.top_k; s0 += 4) {
+__device__ __forceinline__ void slot_gradients(const NormArgs& a, Rows& rows, size_t t, bool live, uint32_t first, PartOf part) {
+    for (uint32_t s0 = first; s0 < a.top_k; s0 += 4) {
         double dot[4] = {0.0, 0.0, 0.0, 0.0};
         part(s0, dot);
-        rows.sum(dot);
-#pragma unroll
-        for (uint32_t s = 0; s < 4; ++s)
-            if (live && threadIdx.x % Rows::kGroup == 0 && s0 + s < a.top_k) a.d_slot_gates[t * a.top_k + s0 + s] = (float)dot[s];
+        slot_sums(a, rows, t, live, s0, dot);
     }
 }
 
@@ -729,7 +735,7 @@ __global__ __launch_bounds__(BLOCK) void block_norm_backward_kernel(NormArgs a) 
             place[u].up(dz[u]);
         }
         if (a.d_slot_gates)
-            slot_gradients(a, rows, t, live, [&](uint32_t s0, double(&dot)[4]) {
+            slot_gradients(a, rows, t, live, 0, [&](uint32_t s0, double(&dot)[4]) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) slot_products<true>(a, t, place[u].from, s0, dz[u], dot);
             });
@@ -770,8 +776,9 @@ __global__ __launch_bounds__(BLOCK) void block_norm_backward_kernel(NormArgs a) 
 // Longer rows, read twice: the sums first, with those of D * w_post * z taken
 // apart into sums that need no D (2000 x 8192 with a pass of its own for them
 // 235 -> 200 us); the columns' sums are kept in LDS (IN_LDS: 200 -> 166 us) or in
-// the block's partial rows, each column by one thread.
-template <bool IN_LDS>
+// the block's partial rows, each column by one thread.  SLOTS: d_slot_gates, the
+// first four of them in the second pass (without them 166 -> 152 us).
+template <bool IN_LDS, bool SLOTS>
 __global__ __launch_bounds__(kLongBlock) void block_norm_backward_long_kernel(NormArgs a) {
     constexpr bool WHOLE = false;
     using Rows = RowGroup<kLongBlock, kLongBlock>;
@@ -780,7 +787,7 @@ __global__ __launch_bounds__(kLongBlock) void block_norm_backward_long_kernel(No
     const uint32_t h = a.hidden, step = kLongBlock * kUnit, first = threadIdx.x * kUnit;
     extern __shared__ float4 lds_sums[];  // [3][units of a row]
     const uint32_t units = (h + kUnit - 1) / kUnit;
-    float* mine = a.partial + (size_t)blockIdx.x * 3 * h;
+    float *mine = a.partial + (size_t)blockIdx.x * 3 * h, *rest = a.rest + (size_t)blockIdx.x * h;
     const float zeros[kUnit] = {};
     for (uint32_t i = first; i < h; i += step)
         for (uint32_t which = 0; which < 3; ++which) {
@@ -848,6 +855,7 @@ __global__ __launch_bounds__(kLongBlock) void block_norm_backward_long_kernel(No
             for (int j = 0; j < kUnit; ++j) now[j] += (float)by[j];
             store_f32<WHOLE>(to, i, h, now);
         };
+        double dots[4] = {0.0, 0.0, 0.0, 0.0};  // of the first four slots
         for (uint32_t i = first; i < h; i += step) {
             read(i);
             double d[kUnit], by[kUnit];
@@ -860,28 +868,43 @@ __global__ __launch_bounds__(kLongBlock) void block_norm_backward_long_kernel(No
             store_f32<WHOLE>(a.d_x + t * h, i, h, v);
             add(kSumPre, 0, i, by);
             if (!a.y) continue;
-            double by_gate[kUnit];
+            double by_gate[kUnit], dz[kUnit];
 #pragma unroll
             for (int j = 0; j < kUnit; ++j) {
                 const double e = token * (double)g[j] * d[j];
-                v[j] = (float)(inv_z * (e * (double)wp[j] - z[j] * back_z));
+                dz[j] = inv_z * (e * (double)wp[j] - z[j] * back_z);
+                v[j] = (float)dz[j];
                 by[j] = e * z[j] * inv_z;
                 by_gate[j] = d[j] * (double)wp[j] * z[j] * inv_z;
             }
             store_f32<WHOLE>(a.d_z + t * h, i, h, v);
+            if constexpr (SLOTS) {
+                slot_products<WHOLE>(a, t, i, 0, dz, dots);
+                if (a.top_k > 4) {
+#pragma unroll
+                    for (int j = 0; j < kUnit; ++j) v[j] = (float)(dz[j] - (double)v[j]);
+                    store_f32<WHOLE>(rest, i, h, v);
+                }
+            }
             add(kSumPost, 1, i, by);
             add(kSumGate, 2, i, by_gate);
         }
-        if (a.d_slot_gates)
-            slot_gradients(a, rows, t, true, [&](uint32_t s0, double(&dot)[4]) {
-                for (uint32_t i = first; i < h; i += step) {  // d_z as it was stored, zeros past the row
+        if constexpr (SLOTS) {
+            slot_sums(a, rows, t, true, 0, dots);
+            // further ones from d_z as it was stored and what that left of it, zeros past the row: of a d_z rounded to f32
+            // alone, the products with a slot that the norm scales out again cancel but for eps, and leave its rounding
+            slot_gradients(a, rows, t, true, 4, [&](uint32_t s0, double(&dot)[4]) {
+                for (uint32_t i = first; i < h; i += step) {
+                    float less[kUnit];
                     widen(kDtypeF32, raw_of<WHOLE>(kDtypeF32, a.d_z, t, i, h), v);
+                    widen(kDtypeF32, raw_of<WHOLE>(kDtypeF32, rest, 0, i, h), less);
                     double dz[kUnit];
 #pragma unroll
-                    for (int j = 0; j < kUnit; ++j) dz[j] = (double)v[j];
+                    for (int j = 0; j < kUnit; ++j) dz[j] = (double)v[j] + (double)less[j];
                     slot_products<WHOLE>(a, t, i, s0, dz, dot);
                 }
             });
+        }
     }
     if constexpr (IN_LDS)
         for (uint32_t i = first; i < h; i += step)
@@ -969,6 +992,15 @@ uint32_t back_blocks(const eidm_norm_shape* s) {
     return need < kBackBlocks ? need : kBackBlocks;
 }
 
+// Rows that no block holds, which are read twice.
+bool back_long(uint32_t hidden) { return hidden < kUnit || hidden > 4096; }
+
+// Scratch: the blocks' column sums, then the rests of the rows that are read twice.
+uint64_t back_sums_bytes(const eidm_norm_shape* s) { return round256((uint64_t)back_blocks(s) * 3 * s->hidden * 4); }
+uint64_t back_scratch_bytes(const eidm_norm_shape* s) {
+    return back_sums_bytes(s) + (back_long(s->hidden) ? round256((uint64_t)back_blocks(s) * s->hidden * 4) : 0);
+}
+
 }  // namespace
 }  // namespace eidm
 
@@ -1029,7 +1061,7 @@ int eidm_block_norm(const eidm_norm_shape* shape, const void* x, const float* y,
 uint64_t eidm_block_norm_backward_scratch_bytes(const eidm_norm_shape* shape) {
     if (check_norm(shape) != EIDM_OK) return 0;
     api_ok();
-    return round256((uint64_t)back_blocks(shape) * 3 * shape->hidden * 4);
+    return back_scratch_bytes(shape);
 }
 
 int eidm_block_norm_backward(const eidm_norm_shape* shape, const void* stream_rows, const float* y,
@@ -1055,7 +1087,7 @@ int eidm_block_norm_backward(const eidm_norm_shape* shape, const void* stream_ro
         !is_aligned(d_w_post, 4) || !is_aligned(d_w_pre, 4))
         return api_fail(EIDM_E_ALIGN, "buffers must be aligned to their scalars");
     const uint32_t blocks = back_blocks(shape);
-    const uint64_t need = round256((uint64_t)blocks * 3 * shape->hidden * 4);
+    const uint64_t need = back_scratch_bytes(shape);
     if (!scratch || scratch_bytes < need)
         return api_fail(EIDM_E_SIZE, "the gradients need %llu bytes of scratch, got %llu", (unsigned long long)need,
                         (unsigned long long)(scratch ? scratch_bytes : 0));
@@ -1073,6 +1105,7 @@ int eidm_block_norm_backward(const eidm_norm_shape* shape, const void* stream_ro
     a.d_slot_gates = d_slot_gates;
     a.d_gate = d_gate;
     a.partial = static_cast<float*>(scratch);
+    a.rest = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + back_sums_bytes(shape));
     const bool channel = d_gate && shape->gate_layout == EIDM_GATE_CHANNEL;
     a.sums = (d_w_pre ? kSumPre : 0) | (d_w_post ? kSumPost : 0) | (channel ? kSumGate : 0);
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1082,19 +1115,19 @@ int eidm_block_norm_backward(const eidm_norm_shape* shape, const void* stream_ro
     auto read_twice = [&] {
         block = kLongBlock;
         lds = 3 * ((h + kUnit - 1) / kUnit) * (uint32_t)sizeof(float4);
-        if (lds <= kLongLds) return go(block_norm_backward_long_kernel<true>);
-        lds = 0;
-        go(block_norm_backward_long_kernel<false>);
+        const bool in_lds = lds <= kLongLds;
+        if (!in_lds) lds = 0;
+        if (d_slot_gates) in_lds ? go(block_norm_backward_long_kernel<true, true>) : go(block_norm_backward_long_kernel<false, true>);
+        else in_lds ? go(block_norm_backward_long_kernel<true, false>) : go(block_norm_backward_long_kernel<false, false>);
     };
     auto by_length = [&](auto whole) {
         constexpr bool W = decltype(whole)::value;
-        if (h < kUnit) return read_twice();
+        if (back_long(h)) return read_twice();
         if (h <= 256) return go(block_norm_backward_kernel<64, kBackBlock, 1, W>);
         if (h <= 512) return go(block_norm_backward_kernel<64, kBackBlock, 2, W>);
         if (h <= 1024) return go(block_norm_backward_kernel<256, kBackBlock, 1, W>);
         if (h <= 2048) return go(block_norm_backward_kernel<512, kBackBlock, 1, W>);
-        if (h <= 4096) return go(block_norm_backward_kernel<512, kBackBlock, 2, W>);
-        read_twice();
+        go(block_norm_backward_kernel<512, kBackBlock, 2, W>);
     };
     if (h % kUnit == 0) by_length(std::true_type{});
     else by_length(std::false_type{});
