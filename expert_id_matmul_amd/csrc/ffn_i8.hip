@@ -130,7 +130,8 @@ int check_ffn(const eidm_ffn_i8_shape* s, FfnI8Plan* p) {
 
 bool ffn_i8_direct(const eidm_ffn_i8_shape* s) {
     return s->top_k <= kI8DownTopK &&
-           i8_rows_by_themselves(s->m, s->top_k, s->n_experts, 3ull * s->hidden * s->inter);
+           i8_rows_by_themselves(s->m, s->top_k, s->n_experts, 3ull * s->hidden * s->inter,
+                                 2 * i8_row_bytes(s->inter, s->hidden) + i8_row_bytes(s->hidden, s->inter));
 }
 
 bool direct_grid_fits(const eidm_ffn_i8_shape* s) {

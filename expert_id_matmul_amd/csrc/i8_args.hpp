@@ -37,7 +37,10 @@ MapBuffers i8_map_at(const eidm_i8_shape* shape, void* scratch);
 // Rows by themselves or tiles, by what is read: sharing saves the reads of every
 // routed row beyond its expert's first, and costs the map and more launches,
 // the time of reading some 64 MB.  (Experts are counted as if picks were even.)
-bool i8_rows_by_themselves(uint32_t m, uint32_t top_k, uint32_t n_experts, uint64_t expert_bytes);
+// row_bytes: what a row's reads cost by themselves, where a load is a whole
+// wavefront's however short k is.
+uint64_t i8_row_bytes(uint32_t n, uint32_t k);
+bool i8_rows_by_themselves(uint32_t m, uint32_t top_k, uint32_t n_experts, uint64_t expert_bytes, uint64_t row_bytes);
 // The same with one weight for all rows, which stays in the caches.
 bool i8_dense_rows_by_themselves(uint32_t m, uint32_t n, uint32_t k, bool whole_units);
 // Rows by themselves read their weights past the caches: most are read once, and more than the caches keep to the next call.

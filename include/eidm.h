@@ -578,8 +578,10 @@ int eidm_quantize_rows(int dtype, uint32_t rows, uint32_t k, const void* x, int8
  * that is written.
  * Grouped reads an expert's weights once for a tile of its rows; AUTO takes it
  * (where it has the scratch it needs) once Direct would read more than some
- * 64 MB again, with picks spread evenly, or with one weight for all rows once
- * there are more than some ten.
+ * 64 MB again, with picks spread evenly and rows of the weights below 512
+ * bytes counted as 512.  With one weight for all rows it takes it once
+ * (m - 1) * n * max(k, 1024) is above 36e3 * k (75e3 * k where k is no
+ * multiple of 16): with n = 4096 from ten rows on, with fewer columns later.
  * Limits: n_experts <= 2048, k <= EIDM_I8_MAX_K, m*top_k and n < 2^31, and
  * (m*top_k / 16 + n_experts + 1) * ceil(n / 64) < 2^31 (EIDM_E_UNSUPPORTED).
  */
