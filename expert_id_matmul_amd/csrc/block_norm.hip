@@ -14,12 +14,14 @@
 //   d_w_post = sum_t v * z * rstd(z),  d_w_pre = sum_t d_normed * out * rstd(out)
 //
 // Bound by memory: every input is read once and every output written once; a
-// row stays in registers between its reductions (rows longer than a block holds
-// are read again).  A row's values and sums are 64-bit, each output is rounded
-// once: an 8-bit value next to a border would otherwise move by a whole step
-// with the order of a sum, and on CDNA4 a 64-bit fma issues at the rate of an
-// f32 one, so the loads still bound: 8 slots of 2048 x 2048 (155 MB) 30.9 us,
-// 5.0 TB/s; gradients of 4096 x 2048 (185 MB) 40.0 and 5.3 for the column sums.
+// row stays in registers between its reductions.  (Rows longer than a block
+// holds are read again, and the slots of a row of any length for d_slot_gates,
+// from the L2: 8 slots of 2048 x 2048 65 us of gradients, 42 at a copy's rate.)
+// A row's values and sums are 64-bit, each output is rounded once: an 8-bit
+// value next to a border would otherwise move by a whole step with the order of
+// a sum, and on CDNA4 a 64-bit fma issues at the rate of an f32 one, so the
+// loads still bound: 8 slots of 2048 x 2048 (155 MB) 30.9 us, 5.0 TB/s;
+// gradients of 4096 x 2048 (185 MB) 39.8 and 5.2 for the column sums.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

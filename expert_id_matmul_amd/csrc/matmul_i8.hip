@@ -325,7 +325,9 @@ bool i8_read_once(uint32_t m, uint32_t top_k, uint32_t n_experts, uint64_t exper
 
 bool i8_one_supported(const I8Args& a, int device_cus) {
     // as many blocks as route and quantise again for less than a launch takes. us, this : routing in a launch of its
-    // own, 2048 x 768, 8 of 128: one token 13.8 : 17.5, 2 20.5 : 21.7, 4 36.3 : 37.3, 8 65.4 : 63.0; 256 x 96, 4 of 16: one 14.1 : 17.4
+    // own, 2048 x 768, 8 of 128: one token 13.8 : 17.5, 2 20.5 : 21.7, 4 36.3 : 37.3, 8 65.4 : 63.0; 256 x 96, 4 of 16: one 14.1 : 17.4.
+    // Many experts are more routing a block: 512 x 128, 8 of 2048, one 19.5 : 22.9; 256 x 128, 8 tokens (1024 blocks) 8 of
+    // 256 14.0 : 14.0, of 512 16.5 : 15.7, of 1024 21.2 : 18.3, of 2048 31.3 : 25.6
     const uint64_t blocks = (uint64_t)a.m * a.top_k * ((a.n + 7) / 8);
     return a.k <= kI8OneRow && blocks <= (uint64_t)device_cus * 16;
 }
@@ -351,7 +353,8 @@ hipError_t launch_i8_gate_up_one(const I8OneArgs& o, hipStream_t stream) {
 
 hipError_t launch_i8_down_combine(const I8DownArgs& a, hipStream_t stream) {
     // up to 8 slots: 16 columns' loads in flight (4 : 8 : 16 columns 40.0 : 42.0 : 37.4 us for the FFN of one token of 8
-    // of 256 experts of 4096 x 1536); twice the wavefronts have half the registers each
+    // of 256 experts of 4096 x 1536, 256 blocks of 16; not measured where fewer columns leave compute units without a
+    // block); twice the wavefronts have half the registers each
     const bool few = a.top_k <= 8;
     const uint32_t cols = few ? 16 : 8, groups = (a.n + cols - 1) / cols, block = 64 * a.top_k;
     const uint64_t grid = (uint64_t)groups * a.m;

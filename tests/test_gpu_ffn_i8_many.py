@@ -1,5 +1,5 @@
-"""The expert FFN in 8 bits (eidm_moe_ffn_i8) of more tokens than its first
-launch has blocks for at four threads' worth of 2^32."""
+"""The expert FFN in 8 bits (eidm_moe_ffn_i8) of more tokens than a launch of
+2^32 threads has blocks for, one to quantise each and one to route four."""
 import pytest
 import torch
 
