@@ -362,16 +362,18 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_kernel(BalanceArgs
     float* mine = picks[wave];
 #pragma unroll
     for (int v = 0; v < NV; ++v) mine[v * 64 + lane] = 0.0f;
+    // the loads' distances from 1: p adds up to 1, so that load - sum load * p is the same of them, and of nearly even
+    // loads nothing cancels (even ones have exactly no gradient)
     float load[NV], w = 0.0f;
     auto fetch = [&] {
         const uint32_t tokens = end - begin;
         const double share = tokens ? 1.0 / (double)tokens : 0.0;
         w = (float)((double)d_loss * (a.coefficient / (double)a.n_seqs) * share);
-        const float per = (float)((double)n / (double)k * share);
+        const double even = (double)k * (double)tokens, per = share / (double)k;  // even picks are even / n
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const uint32_t e = Experts<NV>::of(v);
-            load[v] = e < n ? (float)a.counts[(size_t)q * n + e] * per : 0.0f;
+            load[v] = e < n ? (float)(((double)a.counts[(size_t)q * n + e] * (double)n - even) * per) : 0.0f;
         }
     };
     fetch();

@@ -137,3 +137,31 @@ def test_more_than_2_to_the_30_tokens(lib):
         s = torch.sigmoid(logits[lo:lo + (1 << 26)].double())
         want = d_gates[lo:lo + (1 << 26)].double() * s * torch.sigmoid(-logits[lo:lo + (1 << 26)].double())
         assert ((got[lo:lo + (1 << 26)].double() - want).abs() <= (SLOPE + 2) * ULP * want.abs() + 1e-30).all()
+
+
+@pytest.mark.parametrize("uneven", [0, 1, 40])
+@pytest.mark.parametrize("experts", [16, 200])
+def test_even_loads_leave_no_rounding(lib, experts, uneven):
+    """Probabilities add up to one: the loss's gradient is of the loads' distances from one, none with even picks."""
+    c = Case(lib, 400, experts, 4, [0, 400], True, 1.0)
+    c.ids = torch.arange(1600).remainder(experts).view(400, 4).int()
+    c.ids.view(-1)[:uneven] = (c.ids.view(-1)[:uneven] + 3) // 2
+    counts = c.forward()[0]
+    got = c.backward(counts, gates=False)
+    _, _, _, want, _ = c.formula(gates=False)
+    if not uneven:
+        assert (got == 0).all()
+    s = torch.sigmoid(c.logits.double())
+    p = s / s.sum(1, keepdim=True)
+    off = (counts.double() * experts / 1600 - 1).abs()
+    size = float(c.d_loss) / 400 * (off + (p * off).sum(1, keepdim=True)) * p * (1 - s)
+    near(got, want, (4 * SCORE + 3 * DEPTH + SLOPE + 8) * ULP * size + 1e-18)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(7 * 49, 49, 3), (6 * 110, 110, 7), (29 * 13, 13, 11), (23 * 6, 18, 3)])
+def test_even_loads_of_any_size_have_no_gradient(lib, tokens, experts, top_k):
+    c = Case(lib, tokens, experts, top_k, [0, tokens], True, 1.0)
+    c.ids = torch.arange(tokens * top_k).remainder(experts).view(tokens, top_k).int()
+    counts = c.forward()[0]
+    assert (counts == tokens * top_k // experts).all()
+    assert (c.backward(counts, gates=False) == 0).all()
