@@ -52,8 +52,6 @@ BY_IDS = {
 @pytest.mark.parametrize("name", BY_IDS)
 def test_tiles_by_ids(lib, name, k, slotted):
     tile, experts, m, top_k, n, share = BY_IDS[name]
-    if slotted and "past" in name:
-        pytest.skip("shared rows cover it")
     c = Call(lib, m, n, k, top_k, experts, slotted, "mixed")
     g = np.random.default_rng(m + k)
     flat = 1 + g.integers(0, experts - 1, m * top_k)
